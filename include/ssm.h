@@ -344,6 +344,189 @@ ssm_status ssm_scan_fwd_ckpt(const ssm_desc *desc, const void *u, const void *de
  * (0 when invalid or d_state > 16).  Host-only. */
 size_t ssm_scan_ckpt_bytes(const ssm_desc *desc);
 
+/* ------------------------------------------------------- layer operators
+ * The rest of a scan layer between its two projections, token-major as the
+ * projections leave it: the scan over heads, the short convolution in front
+ * of it, and the root-mean-square norm before and behind.  The conventions at
+ * the head of this file hold, except for layouts:
+ *   - Activations have the token as their second index and the channels of a
+ *     token side by side.  Inputs may be columns of a wider matrix: a
+ *     descriptor holds, in elements, the distance from one batch row and from
+ *     one token to the next (>= 0).  Outputs are dense.  16-byte aligned
+ *     rows of a multiple of 16 bytes are read fastest; none is required.
+ *   - Gradients of activations have io_dtype, gradients of parameters and
+ *     states are float32.
+ *   - n_seqs > 0: sequences packed behind one another in one batch row, with
+ *     cu_seqlens as in ssm_scan_fwd_ex, except that cu_seqlens[n_seqs] may be
+ *     less than seqlen: tokens behind it are not read, and their outputs are
+ *     left as they were.  cu_seqlens is given exactly when n_seqs > 0.
+ *   - A NaN or infinity in u, B, C or dy may reach other tokens of the same
+ *     chunk (64 tokens) and sequence, earlier ones too: masked products are
+ *     multiplied by zero.  It never reaches another sequence.
+ *   - All sums run in a fixed order: results are identical from run to run.
+ *   - flags and reserved must be 0.
+ * Errors are those of the status list, before anything is launched. */
+
+/* ---- The scan over heads: one decay a head and token, B and C shared by the
+ * heads of a group (head h is in group h / (heads / groups)), a state of
+ * head_dim x d_state a head:
+ *   dt_t = softplus(delta_t + delta_bias)   (softplus 0: delta_t + delta_bias)
+ *   h_t = exp(dt_t A) h_{t-1} + dt_t u_t (x) B_t,   y_t = h_t C_t + D u_t
+ * No gate: ssm_norm_fwd applies it. */
+#define SSM_MAX_HEAD_DIM 256
+#define SSM_MAX_HEADS 65535
+typedef struct ssm_heads_desc {
+    int64_t batch, seqlen;         /* seqlen is ignored by ssm_heads_update */
+    int64_t heads, head_dim;       /* 1..65535, 1..256 */
+    int64_t groups;                /* divides heads */
+    int64_t d_state;               /* 1..256 */
+    int64_t n_seqs;                /* packed sequences, 0: every batch row is one */
+    int64_t u_batch_stride, u_token_stride;
+    int64_t delta_batch_stride, delta_token_stride;
+    int64_t B_batch_stride, B_token_stride;
+    int64_t C_batch_stride, C_token_stride;
+    int64_t dy_batch_stride, dy_token_stride;   /* backward only */
+    int32_t io_dtype;              /* ssm_dtype of u, delta, B, C, y, dy, du, ddelta, dB, dC */
+    int32_t softplus;
+    void *workspace;               /* device scratch, 16-byte aligned */
+    size_t workspace_bytes;
+    uint32_t flags, reserved;
+} ssm_heads_desc;
+
+/* Bytes of workspace that ssm_heads_fwd (backward 0) or ssm_heads_bwd (1)
+ * needs; 0 for none, or an invalid descriptor.  Host-only. */
+size_t ssm_heads_workspace_bytes(const ssm_heads_desc *desc, int backward);
+
+/* Forward.
+ *   u              (batch, seqlen, heads, head_dim);  delta (batch, seqlen, heads)
+ *   B, C           (batch, seqlen, groups, d_state)
+ *   A              (heads) float32;  D, delta_bias (heads) float32 or NULL
+ *   initial_state  (rows, heads, head_dim, d_state) float32 or NULL (zeros);
+ *                  rows = batch, or n_seqs
+ *   y              as u, dense, written
+ *   last_state     as initial_state, written, or NULL */
+ssm_status ssm_heads_fwd(const ssm_heads_desc *desc, const void *u, const void *delta,
+                         const float *A, const void *B, const void *C, const float *D,
+                         const float *delta_bias, const float *initial_state,
+                         const int32_t *cu_seqlens, void *y, float *last_state,
+                         ssm_stream_t stream);
+
+/* Gradients of sum(dy * y) + sum(dlast * last_state); dlast may be NULL.  The
+ * states are computed again: nothing of the forward call is needed.
+ *   du (as u), ddelta (of the raw delta), dB, dC: dense, io_dtype, written
+ *   dA (heads), dD, ddelta_bias (heads) or NULL, dh0 (as initial_state) or
+ *   NULL: float32, written
+ * batch is at most 65535. */
+ssm_status ssm_heads_bwd(const ssm_heads_desc *desc, const void *u, const void *delta,
+                         const float *A, const void *B, const void *C, const float *D,
+                         const float *delta_bias, const float *initial_state,
+                         const int32_t *cu_seqlens, const void *dy, const float *dlast, void *du,
+                         void *ddelta, float *dA, void *dB, void *dC, float *dD,
+                         float *ddelta_bias, float *dh0, ssm_stream_t stream);
+
+/* One token of each of `batch` rows, the batch strides alone giving the rows.
+ *   state  (n_slots, heads, head_dim, d_state) float32, updated in place
+ *   slots  (batch) device int32: the state of each row, or NULL: row i is slot
+ *          i (then batch <= n_slots).  A row whose slot is negative or not
+ *          below n_slots is skipped: nothing of it is written.  Slots that
+ *          occur twice give unspecified values in that slot and its rows.
+ *   y      (batch, heads, head_dim) dense, written */
+ssm_status ssm_heads_update(const ssm_heads_desc *desc, float *state, const int32_t *slots,
+                            int64_t n_slots, const void *u, const void *delta, const float *A,
+                            const void *B, const void *C, const float *D, const float *delta_bias,
+                            void *y, ssm_stream_t stream);
+
+/* ---- The short causal depthwise convolution, v_t = bias + sum_k weight[k]
+ * x_{t-(width-1)+k}, y = silu(v) (silu 0: y = v). */
+typedef struct ssm_conv_desc {
+    int64_t batch, seqlen, channels;   /* seqlen is ignored by ssm_conv_update */
+    int64_t n_seqs;
+    int64_t x_batch_stride, x_token_stride;
+    int64_t dy_batch_stride, dy_token_stride;   /* backward only */
+    int32_t width;                     /* taps, 1..SSM_MAX_CONV_WIDTH */
+    int32_t io_dtype;                  /* of x, y, dy, dx */
+    int32_t silu;
+    int32_t reserved;
+    void *workspace;                   /* backward only, 16-byte aligned */
+    size_t workspace_bytes;
+    uint64_t flags;
+} ssm_conv_desc;
+
+/* Bytes of workspace that ssm_conv_bwd needs.  Host-only. */
+size_t ssm_conv_workspace_bytes(const ssm_conv_desc *desc);
+
+/* Forward.
+ *   x            (batch, seqlen, channels)
+ *   weight       (channels, width) float32, the last column on the current
+ *                token;  bias (channels) float32 or NULL
+ *   conv_state   (rows, channels, width - 1) float32 or NULL (zeros): the
+ *                inputs before each sequence, the last column just before it
+ *   y            as x, dense, written
+ *   last_state   as conv_state, written with the inputs that the sequence's
+ *                next token would need, or NULL */
+ssm_status ssm_conv_fwd(const ssm_conv_desc *desc, const void *x, const float *weight,
+                        const float *bias, const float *conv_state, const int32_t *cu_seqlens,
+                        void *y, float *last_state, ssm_stream_t stream);
+
+/* Gradients of sum(dy * y): dx dense, io_dtype; dweight, dbias (or NULL) and
+ * dconv_state (or NULL) float32. */
+ssm_status ssm_conv_bwd(const ssm_conv_desc *desc, const void *x, const float *weight,
+                        const float *bias, const float *conv_state, const int32_t *cu_seqlens,
+                        const void *dy, void *dx, float *dweight, float *dbias, float *dconv_state,
+                        ssm_stream_t stream);
+
+/* One token of each of `batch` rows: x, y (batch, channels), conv_state
+ * (n_slots, channels, width - 1), which moves on by one in place; slots and
+ * skipped rows as in ssm_heads_update. */
+ssm_status ssm_conv_update(const ssm_conv_desc *desc, float *conv_state, const int32_t *slots,
+                           int64_t n_slots, const void *x, const float *weight, const float *bias,
+                           void *y, ssm_stream_t stream);
+
+/* ---- Root-mean-square norm over groups of a row:
+ *   s = x + residual (rounded to residual_dtype; x alone without a residual)
+ *   g = s silu(z) (s alone without a gate)
+ *   y = g / sqrt(mean of g^2 over the group + eps) * weight
+ * In 8 bits (quant_block > 0): every block of quant_block values of a group
+ * (its last may be short) has scale = max|y| / 448 and holds e4m3 values
+ * (4 exponent, 3 mantissa bits, no infinities) of y / scale, rounded to
+ * nearest even; a block below 2^-100 everywhere has scale 0 and zeros. */
+typedef struct ssm_norm_desc {
+    int64_t rows, d;
+    int64_t group_size;                /* divides d; at most 16384 */
+    int64_t quant_block;               /* 0: y in io_dtype; else >= 16, or >= group_size */
+    int64_t x_stride, z_stride, residual_stride, dy_stride;   /* from row to row */
+    int32_t io_dtype;                  /* x, z, y; backward: z, dy, dz */
+    int32_t residual_dtype;            /* io_dtype or SSM_F32: residual, residual_out;
+                                          backward: x, dresidual, dx */
+    float eps;
+    int32_t reserved;
+    void *workspace;                   /* backward only, 16-byte aligned */
+    size_t workspace_bytes;
+    uint64_t flags;
+} ssm_norm_desc;
+
+/* Bytes of workspace that ssm_norm_bwd needs.  Host-only. */
+size_t ssm_norm_workspace_bytes(const ssm_norm_desc *desc);
+
+/* Forward.
+ *   x, z (or NULL), residual (or NULL)  (rows, d);  weight (d) float32
+ *   y             (rows, d) dense: io_dtype, or bytes with quant_block
+ *   scale         (rows, d / group_size * ceil(group_size / quant_block))
+ *                 float32, written with quant_block
+ *   residual_out  (rows, d) dense, written with s when residual is given; it
+ *                 may be the residual itself where that is dense */
+ssm_status ssm_norm_fwd(const ssm_norm_desc *desc, const void *x, const float *weight,
+                        const void *residual, const void *z, void *y, float *scale,
+                        void *residual_out, ssm_stream_t stream);
+
+/* Gradients of sum(dy * y) + sum(dresidual * s) for x = s, what was normed
+ * (residual_out, or the forward's x): dx is the gradient of x and of the
+ * residual alike, dz (required with z) that of the gate; dense.
+ * dresidual (rows, d) is dense, or NULL.  quant_block must be 0. */
+ssm_status ssm_norm_bwd(const ssm_norm_desc *desc, const void *x, const float *weight,
+                        const void *z, const void *dy, const void *dresidual, void *dx, void *dz,
+                        float *dweight, ssm_stream_t stream);
+
 /* Static, NUL-terminated name of a status code ("unknown status" otherwise). */
 const char *ssm_status_string(int status);
 

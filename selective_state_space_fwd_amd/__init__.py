@@ -105,6 +105,7 @@ def load_library(path: str | os.PathLike | None = None) -> ctypes.CDLL:
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_version.argtypes = []
     lib.ssm_version.restype = ctypes.c_int
+    layer.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -479,3 +480,12 @@ def ssm_state_update(state, u, delta, A, B, C, D=None, z=None, y=None, zoh=False
             _ptr(y), _stream(dev))
     return _issue(prepare, lib.ssm_state_update, desc, args, (state, u, delta, A, B, C, D, z, y),
                   y)
+
+
+# ------------------------------------------------------------ layer operators
+
+from . import layer  # noqa: E402
+from .layer import (ssm_conv_bwd, ssm_conv_fwd, ssm_conv_update, ssm_heads_bwd,  # noqa: E402
+                    ssm_heads_fwd, ssm_heads_update, ssm_norm_bwd, ssm_norm_fwd)
+
+__all__ += layer.__all__

@@ -20,7 +20,11 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = ROOT / "_build"
 LIB = PKG / "libssm.so"
-SOURCES = ["ssm_api.hip", "ssm_scan.hip", "ssm_tscan.hip", "ssm_update.hip", "ssm_bwd.hip"]
+LAYER = PKG / "csrc_layer"
+SOURCES = [CSRC / f for f in ("ssm_api.hip", "ssm_scan.hip", "ssm_tscan.hip", "ssm_update.hip",
+                              "ssm_bwd.hip")]
+SOURCES += [LAYER / f for f in ("layer_api.hip", "layer_heads.hip", "layer_heads_bwd.hip",
+                                "layer_update.hip", "layer_conv.hip", "layer_norm.hip")]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -28,13 +32,13 @@ CFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
-    f"-I{INCLUDE}", f"-I{CSRC}",
+    f"-I{INCLUDE}", f"-I{CSRC}", f"-I{LAYER}",
 ]
 
 
-def _compile(src: str) -> Path:
-    obj = BUILD / (Path(src).stem + ".o")
-    cmd = [HIPCC, *CFLAGS, "-c", str(CSRC / src), "-o", str(obj)]
+def _compile(src: Path) -> Path:
+    obj = BUILD / (src.stem + ".o")
+    cmd = [HIPCC, *CFLAGS, "-c", str(src), "-o", str(obj)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     noise = "'-packed-fp32-ops' is not a recognized feature"
     err = "\n".join(l for l in r.stderr.splitlines() if noise not in l and l.strip())

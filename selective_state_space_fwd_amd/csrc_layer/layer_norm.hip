@@ -1,0 +1,308 @@
+// layer_norm.hip -- root-mean-square norm over groups of a row, with the
+// residual's addition in front, the gate silu(z), and an output in 8 bits
+// with one scale a block:
+//   s = x + residual;  g = s silu(z);  y = g / sqrt(mean g^2 + eps) * weight
+//   q = e4m3(y * 448 / max|y|),  scale = max|y| / 448
+// Every value is read and written once: HBM bounds it.  A workgroup holds one
+// group of a row in registers, so the statistic (float32) and the scale need
+// no second read.
+#include "layer_common.h"
+
+namespace ssm {
+
+// Sum over the workgroup of up to 8 wavefronts; `buf` holds 8 values and is
+// not written again before the next barrier.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// e4m3 bits of four values, round to nearest even, magnitudes above 448 kept
+// at 448 (NaN stays NaN).
+__device__ __forceinline__ float clamp8(float v) { return fabsf(v) > 448.0f ? copysignf(448.0f, v) : v; }
+__device__ __forceinline__ uint32_t pack8(float a, float b, float c, float d) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(clamp8(a), clamp8(b), 0, false);
+    return __builtin_amdgcn_cvt_pk_fp8_f32(clamp8(c), clamp8(d), v, true);
+}
+
+template <class IO, class RT, int VW, int NV>
+__global__ __launch_bounds__(512) void norm_fwd_kernel(NormArgs a) {
+    using T = typename IO::T;
+    extern __shared__ uint32_t lds[];           // 8 sums, then the blocks' largest magnitudes
+    float *red = reinterpret_cast<float *>(lds);
+    uint32_t *most = lds + 8;
+    const int nw = blockDim.x >> 6, tid = threadIdx.x;
+    const int64_t ng = a.d / a.group;
+    const int64_t row = blockIdx.x / ng, g0 = (blockIdx.x % ng) * a.group;
+    const int nblk = a.block ? static_cast<int>((a.group + a.block - 1) / a.block) : 0;
+    for (int i = tid; i < nblk; i += blockDim.x) most[i] = 0;
+
+    float v[NV][VW];
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) v[k][i] = 0.0f;
+        if (e < a.group) {
+            const int64_t c = g0 + e;
+            load_vec<IO, VW>(static_cast<const T *>(a.x) + row * a.x_row + c, v[k]);
+            if (a.residual) {
+                float r[VW];
+                load_vec<RT, VW>(static_cast<const typename RT::T *>(a.residual) + row * a.res_row + c, r);
+#pragma unroll
+                for (int i = 0; i < VW; ++i) v[k][i] += r[i];
+                typename RT::T *o = static_cast<typename RT::T *>(a.residual_out) + row * a.d + c;
+                store_vec<RT, VW>(o, v[k]);
+                // the norm is of the sum as it is kept (the backward reads that)
+                if constexpr (sizeof(typename RT::T) == 2) {
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) {
+                        uint16_t h;
+                        BF16::store(&h, 0, v[k][i]);
+                        v[k][i] = BF16::load(&h, 0);
+                    }
+                }
+            }
+            if (a.z) {
+                float z[VW];
+                load_vec<IO, VW>(static_cast<const T *>(a.z) + row * a.z_row + c, z);
+#pragma unroll
+                for (int i = 0; i < VW; ++i) v[k][i] *= silu_f32(z[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < VW; ++i) sum = __builtin_fmaf(v[k][i], v[k][i], sum);
+        }
+    }
+    sum = wave_sum(sum);
+    if (nw > 1) {
+        if ((tid & 63) == 0) red[tid >> 6] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        for (int w = 0; w < nw; ++w) sum += red[w];
+    } else if (nblk) {
+        __syncthreads();                        // the cleared magnitudes
+    }
+    const float rs = 1.0f / sqrtf(sum / static_cast<float>(a.group) + a.eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+        if (e < a.group) {
+            float w[VW];
+            load_vec<F32, VW>(a.weight + g0 + e, w);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) v[k][i] = v[k][i] * rs * w[i];
+            if (!nblk) {
+                store_vec<IO, VW>(static_cast<T *>(a.y) + row * a.d + g0 + e, v[k]);
+            } else {
+                // bits of non-negative floats order as the floats do, NaN above all
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const uint32_t b = __float_as_uint(v[k][i]) & 0x7fffffffu;
+                    m = b > m ? b : m;
+                }
+                atomicMax(most + e / a.block, m);   // a maximum: no order changes it
+            }
+        }
+    }
+    if (!nblk) return;
+    __syncthreads();
+    uint8_t *q = static_cast<uint8_t *>(a.y) + row * a.d + g0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+        if (e < a.group) {
+            // a block of zeros (or below 2^-100, where 448 / max overflows) has scale 0
+            const float m = __uint_as_float(most[e / a.block]);
+            const float inv = m < 0x1p-100f ? 0.0f : 448.0f / m;
+            if constexpr (VW == 1) {
+                q[e] = static_cast<uint8_t>(pack8(v[k][0] * inv, 0.0f, 0.0f, 0.0f));
+            } else {
+                uint32_t o[VW / 4];
+#pragma unroll
+                for (int i = 0; i < VW; i += 4)
+                    o[i / 4] = pack8(v[k][i] * inv, v[k][i + 1] * inv, v[k][i + 2] * inv,
+                                     v[k][i + 3] * inv);
+                if constexpr (VW == 8) *reinterpret_cast<uint2 *>(q + e) = make_uint2(o[0], o[1]);
+                else *reinterpret_cast<uint32_t *>(q + e) = o[0];
+            }
+        }
+    }
+    for (int i = tid; i < nblk; i += blockDim.x) {
+        const float m = __uint_as_float(most[i]);
+        a.scale[(row * ng + g0 / a.group) * nblk + i] = m < 0x1p-100f ? 0.0f : m / 448.0f;
+    }
+}
+
+// Gradients.  n = g rs, dn = dy weight: dg = rs (dn - n mean(dn n)), with
+// mean(dn n) = rs mean(dn g), so both sums are taken in one pass over the row.
+// A workgroup walks rows nblk apart of one group and keeps dweight of its
+// columns in registers: one partial row of dweight a workgroup.
+template <class IO, class RT, int VW, int NV>
+__global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
+    using T = typename IO::T;
+    using R = typename RT::T;
+    __shared__ float red[2][2][8];
+    const int nw = blockDim.x >> 6, tid = threadIdx.x;
+    const int64_t g0 = blockIdx.y * a.group;
+    float dw[NV][VW];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < VW; ++i) dw[k][i] = 0.0f;
+    int par = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += a.nblk, par ^= 1) {
+        float s[NV][VW], z[NV][VW], dy[NV][VW], gate[NV][VW];
+        float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+#pragma unroll
+            for (int i = 0; i < VW; ++i) { s[k][i] = 0.0f; z[k][i] = 0.0f; dy[k][i] = 0.0f; gate[k][i] = 1.0f; }
+            if (e < a.group) {
+                const int64_t c = g0 + e;
+                float w[VW];
+                load_vec<RT, VW>(static_cast<const R *>(a.x) + row * a.x_row + c, s[k]);
+                load_vec<IO, VW>(static_cast<const T *>(a.dy) + row * a.dy_row + c, dy[k]);
+                load_vec<F32, VW>(a.weight + c, w);
+                if (a.z) {
+                    load_vec<IO, VW>(static_cast<const T *>(a.z) + row * a.z_row + c, z[k]);
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) gate[k][i] = silu_f32(z[k][i]);
+                }
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const float g = s[k][i] * gate[k][i];
+                    sq = __builtin_fmaf(g, g, sq);
+                    dot = __builtin_fmaf(dy[k][i] * w[i], g, dot);
+                }
+            }
+        }
+        sq = wave_sum(sq);
+        dot = wave_sum(dot);
+        if (nw > 1) {
+            if ((tid & 63) == 0) { red[par][0][tid >> 6] = sq; red[par][1][tid >> 6] = dot; }
+            __syncthreads();    // the next row writes the other half
+            sq = dot = 0.0f;
+            for (int w = 0; w < nw; ++w) { sq += red[par][0][w]; dot += red[par][1][w]; }
+        }
+        const float m = 1.0f / static_cast<float>(a.group);
+        const float rs = 1.0f / sqrtf(sq * m + a.eps);
+        const float k2 = rs * rs * m * dot;     // rs mean(dn n), per g
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+            if (e < a.group) {
+                const int64_t c = g0 + e;
+                float w[VW], dx[VW], dz[VW], dr[VW];
+                load_vec<F32, VW>(a.weight + c, w);
+                if (a.dresidual)
+                    load_vec<RT, VW>(static_cast<const R *>(a.dresidual) + row * a.d + c, dr);
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const float g = s[k][i] * gate[k][i];
+                    const float dg = rs * (dy[k][i] * w[i] - k2 * g);
+                    dw[k][i] = __builtin_fmaf(dy[k][i], g * rs, dw[k][i]);
+                    dx[i] = dg * gate[k][i];
+                    if (a.dresidual) dx[i] += dr[i];
+                    const float sg = sigmoid_f32(z[k][i]);
+                    dz[i] = dg * s[k][i] * sg * __builtin_fmaf(z[k][i], 1.0f - sg, 1.0f);
+                }
+                store_vec<RT, VW>(static_cast<R *>(a.dx) + row * a.d + c, dx);
+                if (a.z) store_vec<IO, VW>(static_cast<T *>(a.dz) + row * a.d + c, dz);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+        if (e < a.group) store_vec<F32, VW>(a.part + blockIdx.x * a.d + g0 + e, dw[k]);
+    }
+}
+
+// dweight: the workgroups' partial rows, added in order: 64 columns by 4
+// wavefronts, each a quarter of the rows.
+__global__ __launch_bounds__(256) void norm_reduce_kernel(NormArgs a) {
+    __shared__ float sum[4][64];
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
+    const int w = threadIdx.x >> 6;
+    const int64_t per = (a.nblk + 3) / 4;
+    const int64_t r1 = (w + 1) * per < a.nblk ? (w + 1) * per : a.nblk;
+    float v = 0.0f;
+    if (c < a.d)
+        for (int64_t r = w * per; r < r1; ++r) v += a.part[r * a.d + c];
+    sum[w][threadIdx.x & 63] = v;
+    __syncthreads();
+    if (w == 0 && c < a.d) {
+        const int l = threadIdx.x;
+        a.dweight[c] = (sum[0][l] + sum[1][l]) + (sum[2][l] + sum[3][l]);
+    }
+}
+
+// ------------------------------------------------------------------ launch
+static bool al16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// 16-byte accesses need whole vectors in a group (and a block) and aligned rows.
+static bool norm_vec(const NormArgs &a, int V) {
+    bool ok = a.group % V == 0 && al16(a.weight) && al16(a.x) && a.x_row % V == 0;
+    ok = ok && al16(a.z) && (!a.z || a.z_row % V == 0);
+    ok = ok && al16(a.residual) && (!a.residual || a.res_row % V == 0) && al16(a.residual_out);
+    ok = ok && al16(a.dy) && (!a.dy || a.dy_row % V == 0) && al16(a.dresidual);
+    ok = ok && al16(a.y) && al16(a.dx) && al16(a.dz) && al16(a.part);
+    return ok && a.block % V == 0;
+}
+
+int64_t norm_bwd_blocks(int64_t rows, int64_t d, int64_t group) {
+    const int64_t ng = d / group, want = 1024 / ng < 64 ? 64 : 1024 / ng;
+    return rows < want ? rows : want;
+}
+
+template <class IO, class RT, int VW, int NV>
+static hipError_t norm_go(const NormArgs &a, bool bwd, int threads, hipStream_t s) {
+    const int64_t ng = a.d / a.group;
+    if (!bwd) {
+        const int64_t nblk = a.block ? (a.group + a.block - 1) / a.block : 0;
+        hipLaunchKernelGGL((norm_fwd_kernel<IO, RT, VW, NV>),
+                           dim3(static_cast<unsigned>(a.rows * ng)), dim3(threads),
+                           static_cast<unsigned>(4 * (8 + nblk)), s, a);
+        return hipGetLastError();
+    }
+    if (a.nblk > 0)
+        hipLaunchKernelGGL((norm_bwd_kernel<IO, RT, VW, NV>),
+                           dim3(static_cast<unsigned>(a.nblk), static_cast<unsigned>(ng)),
+                           dim3(threads), 0, s, a);
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((a.d + 63) / 64)), dim3(256),
+                       0, s, a);
+    return hipGetLastError();
+}
+
+template <class IO, class RT, int VW>
+static hipError_t norm_vw(const NormArgs &a, bool bwd, hipStream_t s) {
+    // vectors a lane holds: one up to 256 vectors a group, then the least that
+    // keeps the workgroup within 512 lanes
+    const int64_t nvec = (a.group + VW - 1) / VW;
+    const int nv = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : nvec <= 4096 ? 8 : 32;
+    const int threads = static_cast<int>(((nvec + nv - 1) / nv + 63) / 64 * 64);
+    if (nv == 1) return norm_go<IO, RT, VW, 1>(a, bwd, threads, s);
+    if (nv == 2) return norm_go<IO, RT, VW, 2>(a, bwd, threads, s);
+    if constexpr (VW <= 8)
+        if (nv == 4) return norm_go<IO, RT, VW, 4>(a, bwd, threads, s);
+    if constexpr (VW <= 4)
+        if (nv == 8) return norm_go<IO, RT, VW, 8>(a, bwd, threads, s);
+    if constexpr (VW == 1) return norm_go<IO, RT, VW, 32>(a, bwd, threads, s);
+    return hipErrorInvalidValue;
+}
+
+static hipError_t launch_norm(const NormArgs &a, bool bwd, hipStream_t s) {
+    if (a.bf16 && a.res_bf16)
+        return norm_vec(a, 8) ? norm_vw<BF16, BF16, 8>(a, bwd, s) : norm_vw<BF16, BF16, 1>(a, bwd, s);
+    if (a.bf16)
+        return norm_vec(a, 8) ? norm_vw<BF16, F32, 8>(a, bwd, s) : norm_vw<BF16, F32, 1>(a, bwd, s);
+    return norm_vec(a, 4) ? norm_vw<F32, F32, 4>(a, bwd, s) : norm_vw<F32, F32, 1>(a, bwd, s);
+}
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s) { return launch_norm(a, false, s); }
+hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s) { return launch_norm(a, true, s); }
+
+}  // namespace ssm
