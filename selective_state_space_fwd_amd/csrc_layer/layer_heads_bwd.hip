@@ -13,7 +13,10 @@
 //   E_k = X + sum_{t>=k} r_t + sum_{s<k} p_s + sum_{t>=k} sum_{s<t} Z_ts - sum_{s>=k} sum_{t>s} Z_ts
 //   ddt_s = u_s.v_s + A E_s
 // and X needs no product of its own: a chunk's X plus its p is <gh, h> at its
-// end, which is the next chunk's X plus that one's r.
+// end, which is the next chunk's X plus that one's r.  The rounding errors of
+// r and p gather along the way, and alike for all tokens behind, so they do
+// not cancel in dA: every kAnchor-th chunk X is taken anew from float32 copies
+// of the states.
 //
 // Two walks, one in each direction and both in one launch, keep the state (or
 // gh) in registers and leave it at every chunk, with r and p, which go into
@@ -23,6 +26,8 @@
 #include "layer_mat.h"
 
 namespace ssm {
+
+constexpr float kDirect = 0x1p-13f;
 
 // ------------------------------------------------------------------ the walks
 // DIR 0: state from u and B, dotted with C and dy.  DIR 1 (against time): gh
@@ -131,7 +136,33 @@ __global__ __launch_bounds__(256) void heads_walk_kernel(HeadsArgs a, int vecs) 
         const float dt = lane < Q ? step_size<IO>(a, k, lane, h) : 0.0f;
         const double s = lane_prefix(static_cast<double>(dt) * A2);
         const double sQ = __shfl(s, 63, 64);
+        const float dec = exp2_d(sQ);
         ldec += sQ;
+        if (FULL && !idle && k.first) {
+            // the product with the start state, where there is one
+            if (sizeof(E) == 2 && dir == 1 && a.h0) {
+                float v = 0.0f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = 16 * nt + 4 * g + i;
+                        if (n < a.N && l < cols)
+                            v = __builtin_fmaf(S[nt][i],
+                                               a.h0[((k.row * a.H + h) * a.P + p0 + l) * a.N + n], v);
+                    }
+#pragma unroll
+                for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+                if (lane == 0) a.hdot[k.row * slices + slice] = v;
+            }
+        } else if (FULL && sizeof(E) == 2 && !idle && c % kAnchor == 0 && dec >= kDirect) {
+            f4 *to = reinterpret_cast<f4 *>(a.anchor) +
+                     (((dir * a.batch + b) * a.na + c / kAnchor) * slices + slice) * NT * 64 + lane;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) to[nt * 64] = S[nt];
+        }
+        if (FULL && sizeof(E) == 2 && dir == 0 && !idle && p0 == 0 && lane == 0)
+            a.through[(b * a.nc + c) * a.H + h] = dec;
         if (lane < Q) {
             const float up = exp2_d(s), down = exp2_d(sQ - s);
             // behind the chunk's end the staged rows are zero, whatever the weight
@@ -196,7 +227,6 @@ __global__ __launch_bounds__(256) void heads_walk_kernel(HeadsArgs a, int vecs) 
             if (lane == 0 && !idle) a.rpsum[(dir * chunks + b * a.nc + c) * slices + slice] = total;
         }
         // ---- the chunk's tokens join
-        const float dec = exp2_d(sQ);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) S[nt] *= dec;
 #pragma unroll
@@ -217,24 +247,7 @@ __global__ __launch_bounds__(256) void heads_walk_kernel(HeadsArgs a, int vecs) 
                 for (int z = 0; z < M::kTerms; ++z) S[nt] = M::mma(kf, wf[z], S[nt]);
             }
         }
-        if (FULL && dir == 1 && k.first) {
-            if (a.dh0) store_state(a.dh0, k.row);
-            if (a.h0) {
-                float v = 0.0f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int n = 16 * nt + 4 * g + i;
-                        if (n < a.N && l < cols)
-                            v = __builtin_fmaf(S[nt][i],
-                                               a.h0[((k.row * a.H + h) * a.P + p0 + l) * a.N + n], v);
-                    }
-#pragma unroll
-                for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-                if (lane == 0 && !idle) a.hdot[k.row * slices + slice] = v;
-            }
-        }
+        if (FULL && dir == 1 && k.first && a.dh0) store_state(a.dh0, k.row);
         __syncthreads();
     }
     if constexpr (!FULL) {
@@ -244,10 +257,29 @@ __global__ __launch_bounds__(256) void heads_walk_kernel(HeadsArgs a, int vecs) 
     }
 }
 
-// X of every chunk of one head of one batch row, a lane a chunk: the sum of
-// p of the chunks before it less r of those up to it, from <gh, h> of the
-// sequence's start.  Where the chunk keeps less than 2^-24 of its state X is
-// below that share of <gh, h>, and taken as 0: the sum starts anew there.
+// <gh, h_in> of every kAnchor-th chunk that keeps kDirect, a wavefront a head;
+// of no meaning, and not used, where a sequence begins.
+__global__ __launch_bounds__(64) void heads_anchor_kernel(HeadsArgs a, int np) {
+    const int64_t h = blockIdx.x % a.H, x = blockIdx.x / a.H;      // x: batch row and anchor
+    const int64_t sph = (a.P + 15) / 16, per = sph * 4 * np;       // f4s of one head
+    const int64_t all = a.batch * a.na * a.H * per;
+    const int64_t c = x / a.na * a.nc + x % a.na * kAnchor;
+    if (a.through[c * a.H + h] < kDirect) return;
+    const f4 *p = reinterpret_cast<const f4 *>(a.anchor) + (x * a.H + h) * per;
+    double v = 0.0;
+    for (int64_t i = threadIdx.x; i < per; i += 64) {
+        const f4 q = p[i] * p[all + i];
+        v += static_cast<double>((q.x + q.y) + (q.z + q.w));
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    if (threadIdx.x == 0) a.adot[x * a.H + h] = static_cast<float>(v);
+}
+
+// X of every chunk of one head of one batch row, a lane a chunk: itself where
+// a sequence or an anchor gives <gh, h>, else from the chunk before.  Where the
+// chunk keeps less than 2^-24 of its state X is below that share of <gh, h>,
+// and taken as 0: the sum starts anew there.
 __global__ __launch_bounds__(64) void heads_through_kernel(HeadsArgs a) {
     const int lane = threadIdx.x;
     const int64_t h = blockIdx.x, b = blockIdx.y;
@@ -266,14 +298,18 @@ __global__ __launch_bounds__(64) void heads_through_kernel(HeadsArgs a) {
                     r += rs[i];
                     p += rs[chunks * slices + i];
                 }
+                const double keep = a.through[(b * a.nc + c) * a.H + h];   // exp(s_Q)
                 if (k.first) {
                     stop = true;
                     if (a.h0)
                         for (int64_t i = 0; i < sph; ++i) start += a.hdot[k.row * slices + h * sph + i];
-                    start -= r;
-                    if (!a.h0) start = 0.0;
+                    start *= keep;
+                } else if (c % kAnchor == 0 && keep >= kDirect) {
+                    stop = true;
+                    start = keep * a.adot[(b * a.na + c / kAnchor) * a.H + h];
+                } else if (keep < 0x1p-24) {
+                    stop = true;
                 }
-                if (a.through[(b * a.nc + c) * a.H + h] < 0x1p-24f) { stop = true; start = 0.0; }
             } else {
                 stop = true;
             }
@@ -311,7 +347,8 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
     float *es = tok, *we = tok + Q, *rt = tok + 2 * Q, *sd = tok + 3 * Q, *dts = tok + 4 * Q,
           *cx = tok + 5 * Q;                            // cx: TT - 1 rows
     float *colv = tok + (4 + TT) * Q;                   // TRI x 16 each
-    float *rowz = colv + TRI * 16, *diag = rowz + TRI * 16;   // diag: Q
+    float *rowz = colv + TRI * 16, *diag = rowz + TRI * 16, *diagz = diag + Q;   // Q each
+    float *through = diagz + Q;                         // one a wavefront
     E *Ws = Hs;                                         // at the end: Q x LW
 
     const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
@@ -382,6 +419,10 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
                     cx[(q - 1) * Q + lane] = lane < 16 * q ? exp2_d(ref[q] - s) : 0.0f;
             }
         }
+        // X from the staged states themselves: exact in float32; in bfloat16 its
+        // error, 2^-9 of X, is the smaller one where the chunk keeps little
+        const bool direct = sizeof(E) == 4 || exp2_d(sQ) < kDirect;
+        float xdot = 0.0f;
         f4 DX[OWN];
 #pragma unroll
         for (int o = 0; o < OWN; ++o) DX[o] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -427,6 +468,17 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
             stage_rows<IO, PS>(Hs, LB, static_cast<const E *>(a.hin) + so, NP, prow, NP, NP, true);
             stage_rows<IO, PS>(Gs, LB, static_cast<const E *>(a.gout) + so, NP, prow, NP, NP, true);
             __syncthreads();
+            if (direct) {
+                constexpr int V = Seg<IO>::VW;
+                for (int i = threadIdx.x; i < PS * NP / V; i += 256) {
+                    const int at = i / (NP / V) * LB + i % (NP / V) * V;
+                    float x[V], y[V];
+                    load_vec<IO, V>(Hs + at, x);
+                    load_vec<IO, V>(Gs + at, y);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) xdot = __builtin_fmaf(x[e], y[e], xdot);
+                }
+            }
             {   // dy_t . u_s
                 int id = 0;
 #pragma unroll
@@ -564,38 +616,67 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
                             row[i] = v;
                             if (r == q && l == 4 * g + i) {
                                 diag[16 * q + l] = DX[id >> 2][i];          // dy_t . u_t
-                                rowz[TRI * 16 + Q + 16 * q + l] = z[i];     // its share of colv
+                                diagz[16 * q + l] = z[i];                   // its share of colv
                             }
                         }
                         if (l == 0) *reinterpret_cast<f4 *>(rowz + id * 16 + 4 * g) = row;
                     }
         }
+        if (direct) {
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) xdot += __shfl_xor(xdot, o, 64);
+            if (lane == 0) through[wv] = xdot;
+        }
         __syncthreads();
         if (wv == 0) {      // a lane a token
-            float cv = 0.0f, rz = 0.0f, dd = 0.0f, zd = 0.0f, r = 0.0f, p = 0.0f;
+            // E without differences of long sums: of the tiles (q, r) of Z, those
+            // with r < own < q count whole, those of the own row from the token
+            // on, those of the own column up to it; only the tile on the
+            // diagonal is a difference
+            float cv = 0.0f, dd = 0.0f, r = 0.0f, p = 0.0f;
+            double rows = 0.0, cols_ = 0.0, whole = 0.0;
             if (lane < Q) {
-                const int q = lane >> 4;
-                for (int x = q; x < TT; ++x) cv += colv[(x * (x + 1) / 2 + q) * 16 + l];
-                for (int x = 0; x <= q; ++x) rz += rowz[(q * (q + 1) / 2 + x) * 16 + l];
+                const int own = lane >> 4, dg = own * (own + 1) / 2 + own;
+                for (int q = own + 1; q < TT; ++q) {
+                    const int at = q * (q + 1) / 2;
+                    cv += colv[(at + own) * 16 + l];
+                    for (int x = 0; x < own; ++x)
+                        for (int i = 0; i < 16; i += 4) {
+                            const f4 w = *reinterpret_cast<const f4 *>(rowz + (at + x) * 16 + i);
+                            whole += (w.x + w.y) + (w.z + w.w);
+                        }
+                }
+                cols_ = static_cast<double>(cv) * dt;
+                for (int x = 0; x < own; ++x) rows += rowz[(own * (own + 1) / 2 + x) * 16 + l];
+                rows += static_cast<double>(rowz[dg * 16 + l]) -
+                        static_cast<double>(colv[dg * 16 + l] - diagz[lane]) * dt;
+                cv += colv[dg * 16 + l];
                 dd = diag[lane];
-                zd = diag[Q + lane];
                 const float *rp = a.rp + (ci * slices + h * sph) * Q + lane;
                 for (int64_t i = 0; i < sph; ++i) {
                     r += rp[i * Q];
                     p += rp[chunks * slices * Q + i * Q];
                 }
             }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) {      // rows: from the token on; columns: up to it
+                const double x = __shfl_down(rows, o, 16), y = __shfl_up(cols_, o, 16);
+                if (l + o < 16) rows += x;
+                if (l >= o) cols_ += y;
+            }
+            const double before = __shfl_up(cols_, 1, 16);
             const double pd = static_cast<double>(p) * dt;
-            const double f = static_cast<double>(r) + rz - static_cast<double>(cv - zd) * dt;
-            // sum of f over tokens >= k, of p over tokens < k
-            const double fs = lane_prefix(f), ps = lane_prefix(pd);
-            const double E_ = a.through[ci * a.H + h] + (__shfl(fs, 63, 64) - fs + f) + (ps - pd);
+            const double rs = lane_prefix(static_cast<double>(r)), ps = lane_prefix(pd);
+            const float X = direct ? exp2_d(sQ) * ((through[0] + through[1]) + (through[2] + through[3]))
+                                   : a.through[ci * a.H + h];
+            const double E_ = X + (__shfl(rs, 63, 64) - rs + r) + (ps - pd) + whole + rows +
+                              (l ? before : 0.0);
             const float ddt = cv + p + a.A[h] * static_cast<float>(E_);
             float dd_ = 0.0f;
             if (lane < k.n) {
                 float raw = IO::load(static_cast<const E *>(a.delta) + k.b * a.dt_b + (k.t + lane) * a.dt_t, h);
                 if (a.bias) raw += a.bias[h];
-                dd_ = a.softplus ? ddt * sigmoid_f32(raw) : ddt;
+                dd_ = a.softplus ? ddt / (1.0f + expf(-raw)) : ddt;
                 IO::store(static_cast<E *>(a.ddelta) + (k.b * a.L + k.t + lane) * a.H, h, dd_);
             }
             double sA = lane < k.n ? E_ * dt : 0.0, sD = lane < k.n ? dd : 0.0f, sb = dd_;
@@ -664,21 +745,6 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
     }
 }
 
-// exp(s_Q) of every chunk and head, which heads_through_kernel replaces by X.
-template <class IO>
-__global__ __launch_bounds__(256) void heads_decay_kernel(HeadsArgs a) {
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 6;
-    const int lane = threadIdx.x & 63;
-    const int64_t chunks = a.batch * a.nc;
-    if (i >= chunks * a.H) return;
-    const int64_t c = i / a.H, h = i % a.H;
-    const Chunk k = chunk_at(a, c / a.nc, c % a.nc);
-    double v = lane < a.Q ? static_cast<double>(step_size<IO>(a, k, lane, h)) : 0.0;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    if (lane == 0) a.through[i] = exp2_d(v * a.A[h] * kLog2e);
-}
-
 // dA, dD and ddelta_bias: the chunks' shares, added in a fixed order.
 __global__ __launch_bounds__(64) void heads_sums_kernel(HeadsArgs a) {
     const int64_t h = blockIdx.x, chunks = a.batch * a.nc;
@@ -717,7 +783,7 @@ static hipError_t bwd_go(const HeadsArgs &a, hipStream_t s) {
     constexpr int TT = Q / 16, TRI = TT * (TT + 1) / 2;
     constexpr int LB = NP + M::kPad, LU = PS + M::kPad;
     constexpr size_t lds = sizeof(E) * (2 * Q * LB + 2 * Q * LU + 2 * PS * LB + TRI * 256) +
-                           16 * TRI * 64 + 4 * ((4 + TT) * Q + 2 * TRI * 16 + 2 * Q);
+                           16 * TRI * 64 + 4 * ((4 + TT) * Q + 2 * TRI * 16 + 2 * Q + 4);
     static_assert(lds <= 160 * 1024, "LDS of a compute unit");
     static_assert(Q * (Q + M::kPad) <= 2 * PS * LB, "W takes the states' place");
     const int64_t hpg = a.H / a.G, sph = (a.P + 15) / 16;
@@ -737,10 +803,13 @@ static hipError_t bwd_go(const HeadsArgs &a, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, true>), dim3(walks), dim3(256), 0, s, a, vecs);
-    hipLaunchKernelGGL((heads_decay_kernel<IO>), dim3(static_cast<unsigned>((chunks * a.H + 3) / 4)),
-                       dim3(256), 0, s, a);
-    hipLaunchKernelGGL(heads_through_kernel, dim3(static_cast<unsigned>(a.H), static_cast<unsigned>(a.batch)),
-                       dim3(64), 0, s, a);
+    if constexpr (sizeof(E) == 2) {
+        hipLaunchKernelGGL(heads_anchor_kernel, dim3(static_cast<unsigned>(a.batch * a.na * a.H)),
+                           dim3(64), 0, s, a, NP);
+        hipLaunchKernelGGL(heads_through_kernel,
+                           dim3(static_cast<unsigned>(a.H), static_cast<unsigned>(a.batch)), dim3(64), 0,
+                           s, a);
+    }
     hipLaunchKernelGGL((heads_chunk_bwd_kernel<IO, NP, Q, PS>),
                        dim3(static_cast<unsigned>(chunks * a.G * a.hsplit)), dim3(256), lds, s, a, vecs);
     return hipGetLastError();

@@ -61,6 +61,9 @@ int64_t norm_bwd_blocks(int64_t rows, int64_t d, int64_t group);
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s);
 
+// Chunks between two float32 copies of the states in the backward.
+constexpr int kAnchor = 2;
+
 // One chunk of the scan over heads: tokens t .. t + n - 1 of sequence `row`.
 struct HeadsEntry {
     int32_t t, n, row, flags;   // flags: kFirst, kLast chunk of its sequence
@@ -92,7 +95,11 @@ struct HeadsArgs {
                                 // the chunks, gradients of those that leave them
     float *rp;                  // (2, batch nc, H slices, Q) dot products across chunks, see layer_heads_bwd.hip
     float *rpsum;               // (2, batch nc, H slices) their sums over a chunk's tokens
-    float *hdot;                // (rows, H slices) <gradient of the start state, start state>
+    float *hdot;                // (rows, H slices) <gradient leaving a first chunk, start state>
+    float *anchor;              // (2, batch, na, H slices, 16 Np) float32 state entering every
+                                // kAnchor-th chunk, and gradient leaving it
+    float *adot;                // (batch, na, H) their products
+    int64_t na;
     float *through;             // (batch nc, H) exp(s_Q) <gout, hin>
     float *part;                // (3, batch nc, H) dA, dD, ddelta_bias of a chunk
     int64_t hsplit, hblk;       // backward: blocks of hblk heads of a group

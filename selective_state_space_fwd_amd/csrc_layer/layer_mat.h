@@ -163,7 +163,8 @@ __device__ __forceinline__ float step_size(const HeadsArgs &a, const Chunk &k, i
     if (t >= k.n) return 0.0f;
     float v = IO::load(static_cast<const typename IO::T *>(a.delta) + k.b * a.dt_b + (k.t + t) * a.dt_t, h);
     if (a.bias) v += a.bias[h];
-    return a.softplus ? softplus_f32(v) : v;
+    // once a token and head: log1pf and expf, whose errors do not add up in dA
+    return a.softplus ? fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))) : v;
 }
 
 // Inclusive sum over the lanes of a wavefront, in 64 bits: differences of
@@ -179,7 +180,13 @@ __device__ __forceinline__ double lane_prefix(double v) {
     return v;
 }
 
-__device__ __forceinline__ float exp2_d(double x) { return exp2_hw(static_cast<float>(x)); }
+// 2^x of an exponent in 64 bits: what its rounding to float leaves out comes
+// back as a factor 1 + lo ln 2.
+__device__ __forceinline__ float exp2_d(double x) {
+    const float hi = static_cast<float>(x), lo = static_cast<float>(x - hi);
+    const float e = exp2_hw(hi);
+    return __builtin_fmaf(e * kLn2, lo, e);
+}
 
 // Host: whether rows of `src` can be read in 16-byte pieces.
 template <class IO>
