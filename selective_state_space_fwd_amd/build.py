@@ -23,7 +23,8 @@ LIB = PKG / "libssm.so"
 LAYER = PKG / "csrc_layer"
 SOURCES = [CSRC / f for f in ("ssm_api.hip", "ssm_scan.hip", "ssm_tscan.hip", "ssm_update.hip",
                               "ssm_bwd.hip")]
-SOURCES += [LAYER / f for f in ("layer_api.hip", "layer_heads.hip", "layer_heads_bwd.hip",
+SOURCES += [LAYER / f for f in ("layer_api.hip", "layer_heads.hip", "layer_heads_bf16.hip", "layer_heads_f32.hip",
+                                "layer_heads_bwd.hip",
                                 "layer_update.hip", "layer_conv.hip", "layer_norm.hip")]
 
 ARCH = "gfx950"

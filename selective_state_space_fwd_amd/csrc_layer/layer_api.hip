@@ -72,7 +72,7 @@ ssm_status plan_heads(const ssm_heads_desc *d, bool bwd, HeadsPlan *p) {
     const int64_t base = d->batch * p->wgs * (bwd ? 2 : 1);
     p->Kc = p->nc > 0 ? p->nc : 1;
     if (base > 0 && base < 256 && p->nc >= 8) {
-        int64_t J = ceil_div(512, base);
+        int64_t J = ceil_div(768, base);
         if (J > p->nc / 4) J = p->nc / 4;
         p->Kc = ceil_div(p->nc, J);
     }

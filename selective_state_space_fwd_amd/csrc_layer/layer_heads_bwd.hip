@@ -27,6 +27,14 @@
 
 namespace ssm {
 
+// Row in the permuted order out of a row kept in the natural one.
+template <class IO>
+__device__ __forceinline__ typename Mat<IO>::Frag row_nat(const typename IO::T *p, int g) {
+    if constexpr (sizeof(typename IO::T) == 4) return Mat<IO>::row_perm(p, g);
+    else return Mat<IO>::join(*reinterpret_cast<const uint2 *>(p + 4 * g),
+                              *reinterpret_cast<const uint2 *>(p + 16 + 4 * g));
+}
+
 constexpr float kDirect = 0x1p-13f;
 
 // ------------------------------------------------------------------ the walks
@@ -196,7 +204,7 @@ __global__ __launch_bounds__(256) void heads_walk_kernel(HeadsArgs a, int vecs) 
                 for (int z = 0; z < M::kTerms; ++z) hf[z] = M::take(v);
 #pragma unroll
                 for (int q = 0; q < TT; ++q) {
-                    const Frag rf = M::row_perm(Rs + (16 * q + l) * LB + 32 * m, g);
+                    const Frag rf = row_nat<IO>(Rs + (16 * q + l) * LB + 32 * m, g);
 #pragma unroll
                     for (int z = 0; z < M::kTerms; ++z) Y[q] = M::mma(rf, hf[z], Y[q]);
                 }
@@ -556,8 +564,8 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
                     f4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
 #pragma unroll
                     for (int m = 0; m < KP; ++m) {
-                        x = M::mma(M::row_perm(Ys + (16 * q + l) * LU + 32 * m, g), hf[m], x);
-                        y = M::mma(M::row_perm(Us + (16 * q + l) * LU + 32 * m, g), gf[m], y);
+                        x = M::mma(row_nat<IO>(Ys + (16 * q + l) * LU + 32 * m, g), hf[m], x);
+                        y = M::mma(row_nat<IO>(Us + (16 * q + l) * LU + 32 * m, g), gf[m], y);
                     }
                     const f4 e = *reinterpret_cast<const f4 *>(es + 16 * q + 4 * g);
                     const f4 w = *reinterpret_cast<const f4 *>(we + 16 * q + 4 * g) *
@@ -720,7 +728,7 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
             const Frag cf = M::col_perm(Cs + 32 * m * LB + 16 * nt, LB, g, l);
 #pragma unroll
             for (int q = 0; q < TT; ++q) {
-                dC[q][n] = M::mma(M::row_perm(Ws + (16 * q + l) * LW + 32 * m, g), bf, dC[q][n]);
+                dC[q][n] = M::mma(row_nat<IO>(Ws + (16 * q + l) * LW + 32 * m, g), bf, dC[q][n]);
                 dB[q][n] = M::mma(M::col_perm(Ws + 32 * m * LW + 16 * q, LW, g, l), cf, dB[q][n]);
             }
         }

@@ -4,8 +4,12 @@
 // of 16 lanes l): lane (g, l) holds 8 values of k of row (or column) l.  Which
 // 8 does not matter as long as both operands agree, and three orders occur:
 //   row       k = 8g .. 8g+7                     (16 neighbouring bytes)
-//   row_perm  k = 4g .. 4g+3, 16+4g .. 16+4g+3   (two pieces of 8 bytes)
+//   row_perm  k = 4g .. 4g+3, 16+4g .. 16+4g+3
 //   col_perm  the same k, read down a column of a matrix stored by rows of k
+// 16-bit rows that are read in the permuted order are kept so in LDS (pos):
+// one read of 16 bytes instead of two of 8, which run at half the rate at
+// every distance of the rows (measured: 31 .. 37 against 66 cycles for the four
+// wavefronts' 4 KB).
 // A result tile has rows 4g .. 4g+3 of column l in lane (g, l): two result
 // tiles one above the other are an operand in the permuted order, with no
 // data moved between lanes.
@@ -37,16 +41,27 @@ struct Mat<BF16> {
         b.q = *reinterpret_cast<const uint4 *>(p + 8 * g);
         return b.f;
     }
-    static __device__ __forceinline__ Frag row_perm(const E *p, int g) {
-        Bits b;
-        b.d[0] = *reinterpret_cast<const uint2 *>(p + 4 * g);
-        b.d[1] = *reinterpret_cast<const uint2 *>(p + 16 + 4 * g);
-        return b.f;
+    // where column c of a row kept in the permuted order lies; whole tiles of
+    // 16 columns: the tile's first value is at pos, the next fours at pos + 8
+    static __device__ __forceinline__ constexpr int pos(int c) {
+        return (c & ~31) + (c >> 2 & 3) * 8 + (c >> 4 & 1) * 4 + (c & 3);
     }
-    // m: row k = 0, column 0 of the tile; LDS transposes 4 x 16 values a group
+    static __device__ __forceinline__ Frag row_perm(const E *p, int g) { return row(p, g); }
+    // columns c .. c + 7 (c a multiple of 8) into a row kept in that order
+    template <class Vec>
+    static __device__ __forceinline__ void put_perm(E *row, int c, const Vec &v) {
+        uint2 h[2];
+        __builtin_memcpy(h, &v, 16);
+        *reinterpret_cast<uint2 *>(row + pos(c)) = h[0];
+        *reinterpret_cast<uint2 *>(row + pos(c + 4)) = h[1];
+    }
+    // m: row k = 0 and column 0 of the tile; LDS transposes 4 x 16 values a
+    // group.  FOUR: distance of the tile's fours of columns, 8 in rows kept
+    // in the permuted order.
+    template <int FOUR = 4>
     static __device__ __forceinline__ Frag col_perm(const E *m, int stride, int g, int l) {
         using L3 = __attribute__((address_space(3))) s4v;
-        const E *p = m + (4 * g + (l >> 2)) * stride + 4 * (l & 3);
+        const E *p = m + (4 * g + (l >> 2)) * stride + FOUR * (l & 3);
         Bits b;
         b.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L3 *)(p));
         b.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L3 *)(p + 16 * stride));
@@ -61,6 +76,18 @@ struct Mat<BF16> {
         Bits b;
         b.f = f;
         Seg<BF16>::unpack(b.q, v);
+    }
+    // half an operand (one result tile) in LDS: 8 bytes a lane
+    using Half = uint2;
+    static __device__ __forceinline__ Half half(f4 v) {
+        return make_uint2(Seg<BF16>::pk(v.x, v.y), Seg<BF16>::pk(v.z, v.w));
+    }
+    static __device__ __forceinline__ Half none() { return make_uint2(0, 0); }
+    static __device__ __forceinline__ Frag join(Half a, Half b) {
+        Bits x;
+        x.d[0] = a;
+        x.d[1] = b;
+        return x.f;
     }
     // v becomes what packing it left out
     static __device__ __forceinline__ Frag take(float (&v)[8]) {
@@ -89,7 +116,13 @@ struct Mat<F32> {
         return Frag{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     }
     static __device__ __forceinline__ Frag row(const E *p, int g) { return two(p + 8 * g, p + 8 * g + 4); }
+    static __device__ __forceinline__ constexpr int pos(int c) { return c; }
     static __device__ __forceinline__ Frag row_perm(const E *p, int g) { return two(p + 4 * g, p + 16 + 4 * g); }
+    template <class Vec>
+    static __device__ __forceinline__ void put_perm(E *row, int c, const Vec &v) {
+        __builtin_memcpy(__builtin_assume_aligned(row + c, 16), &v, 16);
+    }
+    template <int FOUR = 4>
     static __device__ __forceinline__ Frag col_perm(const E *m, int stride, int g, int l) {
         Frag f;
 #pragma unroll
@@ -102,6 +135,12 @@ struct Mat<F32> {
     static __device__ __forceinline__ void unpack(Frag f, float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = f[i];
+    }
+    using Half = f4;
+    static __device__ __forceinline__ Half half(f4 v) { return v; }
+    static __device__ __forceinline__ Half none() { return f4{0.0f, 0.0f, 0.0f, 0.0f}; }
+    static __device__ __forceinline__ Frag join(Half a, Half b) {
+        return Frag{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     }
     static __device__ __forceinline__ Frag take(float (&v)[8]) { return pack(v); }
 };
@@ -157,27 +196,39 @@ __device__ __forceinline__ void stage_rows(typename IO::T *dst, int ld, const ty
     }
 }
 
-// The step size of one token of one head (0 behind the chunk's end).
-template <class IO>
-__device__ __forceinline__ float step_size(const HeadsArgs &a, const Chunk &k, int t, int64_t h) {
-    if (t >= k.n) return 0.0f;
-    float v = IO::load(static_cast<const typename IO::T *>(a.delta) + k.b * a.dt_b + (k.t + t) * a.dt_t, h);
-    if (a.bias) v += a.bias[h];
-    // once a token and head: log1pf and expf, whose errors do not add up in dA
-    return a.softplus ? fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))) : v;
+// Workgroup id -> position: the ids of one XCD (id % 8) become neighbours, so
+// that the heads that share B and C share an L2.
+__device__ __forceinline__ int64_t by_xcd(int64_t id, int64_t total) {
+    const int64_t x = id & 7, q = total >> 3, r = total & 7;
+    return x * q + (x < r ? x : r) + (id >> 3);
 }
 
 // Inclusive sum over the lanes of a wavefront, in 64 bits: differences of
 // these sums are the exponents, and in 32 bits the chunk's later ones would
-// lose 1e-6 of the decay.
+// lose 1e-6 of the decay.  Four DPP shifts within 16 lanes, then the two
+// broadcasts of a row's last lane to the rows behind it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t b = __double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xf, false);
+    return v + __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);   // 0.0 where nothing comes
+}
 __device__ __forceinline__ double lane_prefix(double v) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double w = __shfl_up(v, o, 64);
-        if (l >= o) v += w;
-    }
+    v = dpp_add<0x111, 0xf>(v);     // row_shr:1, 2, 4, 8
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);     // row_bcast:15 into rows 1 and 3
+    v = dpp_add<0x143, 0xc>(v);     // row_bcast:31 into rows 2 and 3
     return v;
+}
+// The value of one lane, for all.
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t b = __double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+    return __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 // 2^x of an exponent in 64 bits: what its rounding to float leaves out comes
@@ -186,6 +237,23 @@ __device__ __forceinline__ float exp2_d(double x) {
     const float hi = static_cast<float>(x), lo = static_cast<float>(x - hi);
     const float e = exp2_hw(hi);
     return __builtin_fmaf(e * kLn2, lo, e);
+}
+
+// softplus to an ulp or two, as ssm_common.h's but with the exponent in 64 bits:
+// dA adds up the step sizes' errors over all tokens.
+__device__ __forceinline__ float softplus_exact(float x) {
+    const float e = exp2_d(static_cast<double>(-fabsf(x)) * 1.4426950408889634);
+    const float s = 1.0f + e;
+    return fmaxf(x, 0.0f) + __builtin_fmaf(log2_hw(s), kLn2, (1.0f - s) + e);
+}
+
+// The step size of one token of one head (0 behind the chunk's end).
+template <class IO>
+__device__ __forceinline__ float step_size(const HeadsArgs &a, const Chunk &k, int t, int64_t h) {
+    if (t >= k.n) return 0.0f;
+    float v = IO::load(static_cast<const typename IO::T *>(a.delta) + k.b * a.dt_b + (k.t + t) * a.dt_t, h);
+    if (a.bias) v += a.bias[h];
+    return a.softplus ? softplus_exact(v) : v;
 }
 
 // Host: whether rows of `src` can be read in 16-byte pieces.
