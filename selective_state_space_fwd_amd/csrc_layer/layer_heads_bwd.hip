@@ -27,171 +27,277 @@
 
 namespace ssm {
 
-// Row in the permuted order out of a row kept in the natural one.
-template <class IO>
-__device__ __forceinline__ typename Mat<IO>::Frag row_nat(const typename IO::T *p, int g) {
-    if constexpr (sizeof(typename IO::T) == 4) return Mat<IO>::row_perm(p, g);
-    else return Mat<IO>::join(*reinterpret_cast<const uint2 *>(p + 4 * g),
-                              *reinterpret_cast<const uint2 *>(p + 16 + 4 * g));
+// Sum over the 16 lanes of a row, in all of them.
+__device__ __forceinline__ float row_sum(float v) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xf, 0xf, false));  // row_ror:1
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xf, 0xf, false));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xf, 0xf, false));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xf, 0xf, false));
+    return v;
 }
 
 constexpr float kDirect = 0x1p-13f;
 
 // ------------------------------------------------------------------ the walks
+template <class IO, int NP, int Q, bool FULL>
+struct WalkMem {
+    using M = Mat<IO>;
+    using E = typename M::E;
+    static constexpr int LB = NP + M::kPad, LU = 64 + M::kPad;
+    __attribute__((aligned(16))) E K[Q * LB];               // read down its columns
+    __attribute__((aligned(16))) E R[FULL ? Q * LB : 8];    // rows in the permuted order
+    __attribute__((aligned(16))) E X[Q * LU];
+    __attribute__((aligned(16))) E Y[FULL ? Q * LU : 8];
+    __attribute__((aligned(16))) float tok[4][Q];
+};
+
+template <class IO, int NP, int Q, bool FULL>
+constexpr int walk_waves() {
+    constexpr int n = static_cast<int>(160 * 1024 / sizeof(WalkMem<IO, NP, Q, FULL>));
+    constexpr int r = NP > 128 ? 1 : sizeof(typename IO::T) == 4 && FULL ? 2 : 3;
+    return n < 1 ? 1 : n > r ? r : n;
+}
+
 // DIR 0: state from u and B, dotted with C and dy.  DIR 1 (against time): gh
 // from dy and C, dotted with B and u.  FULL false: only the end of a range.
-template <class IO, int NP, int Q, bool FULL>
-__global__ __launch_bounds__(256) void heads_walk_kernel(HeadsArgs a, int vecs) {
+// WIDE: as in the forward walk.
+template <class IO, int NP, int Q, bool FULL, bool WIDE>
+__global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_walk_kernel(HeadsArgs a) {
     using M = Mat<IO>;
     using E = typename M::E;
     using Frag = typename M::Frag;
+    using Mem = WalkMem<IO, NP, Q, FULL>;
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    constexpr int V = Seg<IO>::VW, ES = sizeof(E);
     constexpr int NT = NP / 16, KN = NP / 32, TT = Q / 16, KS = Q / 32;
-    constexpr int LB = NP + M::kPad, LU = 64 + M::kPad;
-    __shared__ __attribute__((aligned(16))) E Ks[Q * LB];
-    __shared__ __attribute__((aligned(16))) E Rs[FULL ? Q * LB : 8];
-    __shared__ __attribute__((aligned(16))) E Xs[Q * LU];
-    __shared__ __attribute__((aligned(16))) E Ys[FULL ? Q * LU : 8];
-    __shared__ __attribute__((aligned(16))) float tok[4][2 * Q];
+    constexpr int LB = Mem::LB, LU = Mem::LU;
+    constexpr int PB = NP / V, NB = Q * PB / 256, PU = 64 / V, NU = Q * PU / 256;
+    static_assert(Q * PB % 256 == 0 && Q * PU % 256 == 0, "whole rounds of the workgroup");
+    __shared__ Mem mem;
 
-    const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-    const int64_t hpg = a.H / a.G, sph = (a.P + 15) / 16, per = (hpg * sph + 3) / 4;
-    const int64_t wgs = a.G * per, half = wgs * a.J * a.batch;
-    const int dir = blockIdx.x >= half;
-    const int64_t id = blockIdx.x - (dir ? half : 0);
-    const int64_t wg = id % wgs, j = (id / wgs) % a.J, b = id / (wgs * a.J);
-    const int64_t gr = wg / per, is = (wg % per) * 4 + wv;
+    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63, g = lane >> 4, l = lane & 15;
+    const int N = static_cast<int>(a.N), P = static_cast<int>(a.P), H = static_cast<int>(a.H);
+    const int hpg = static_cast<int>(a.H / a.G), sph = (P + 15) / 16, per = (hpg * sph + 3) / 4;
+    const int wgs = static_cast<int>(a.G) * per, J = static_cast<int>(a.J);
+    const int half = wgs * J * static_cast<int>(a.batch);
+    const int all = static_cast<int>(by_xcd(blockIdx.x, gridDim.x));
+    const int dir = all >= half, id = all - (dir ? half : 0);
+    const int wg = id % wgs, j = id / wgs % J, b = id / (wgs * J);
+    const int gr = wg / per, is0 = wg % per * 4, is = is0 + wv;
     const bool idle = is >= hpg * sph;
-    const int64_t h = gr * hpg + (idle ? 0 : is / sph);
-    const int p0 = idle ? 0 : static_cast<int>(is % sph) * 16;
-    const int cols = idle ? 0 : static_cast<int>(a.P - p0 < 16 ? a.P - p0 : 16);
-    const float A2 = a.A[h] * kLog2e;
-    float *es = tok[wv], *ws = es + Q;
-    const int64_t Pr = sph * 16, slices = a.H * sph, slice = h * sph + p0 / 16;
-    const int64_t chunks = a.batch * a.nc;
+    const int h = gr * hpg + (idle ? 0 : is / sph), p0 = idle ? 0 : is % sph * 16;
+    const int cols = idle ? 0 : min(P - p0, 16);
+    const double A2 = static_cast<double>(a.A[h]) * 1.4426950408889634;
+    const float bias = a.bias ? a.bias[h] : 0.0f;
+    float *ws = mem.tok[wv];
+    const int64_t slices = a.H * sph, slice = static_cast<int64_t>(h) * sph + p0 / 16;
+    const int64_t chunks = a.batch * a.nc, row0 = b * a.nc;
 
     f4 S[NT];
-    auto load_state = [&](const float *src, int64_t row) {
+    auto state_at = [&](int N_, int nt, int i) -> uint32_t {
+        const int n = 16 * nt + 4 * g + i;
+        return n < N_ && l < cols ? static_cast<uint32_t>((p0 + l) * N_ + n) * 4 : kDrop;
+    };
+    auto state_view = [&](const float *p, int64_t row) {
+        return view(p + (row * H + h) * P * N, 0x7fffffff);
+    };
+    auto load_state = [&](f4 (&to)[NT], const float *src, int64_t row) {
+        const Rsrc r = state_view(src, row);
+        int N_ = N;
+        asm volatile("" : "+s"(N_));            // the offsets are made here, not kept over the walk
+        if ((N_ & 3) == 0) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
+                to[nt] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, state_at(N_, nt, 0), 0, 0));
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = 16 * nt + 4 * g + i;
-                S[nt][i] = src && n < a.N && l < cols
-                               ? src[((row * a.H + h) * a.P + p0 + l) * a.N + n] : 0.0f;
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    to[nt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, state_at(N_, nt, i), 0, 0));
+        }
     };
     auto store_state = [&](float *dst, int64_t row) {
+        const Rsrc r = state_view(dst, row);
+        int N_ = N;
+        asm volatile("" : "+s"(N_));
+        if ((N_ & 3) == 0) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, S[nt]), r, state_at(N_, nt, 0), 0, 0);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = 16 * nt + 4 * g + i;
-                if (n < a.N && l < cols) dst[((row * a.H + h) * a.P + p0 + l) * a.N + n] = S[nt][i];
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[nt][i]), r, state_at(N_, nt, i), 0, 0);
+        }
+    };
+    auto clear_state = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[nt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     };
     float *hend = a.hend + (dir ? a.batch * a.J * a.H * a.P * a.N : 0);
     float *ldecs = a.ldec + (dir ? a.batch * a.J * a.H : 0);
-    if (FULL && dir == 0 && j > 0) load_state(hend, b * a.J + j - 1);
-    else if (FULL && dir == 1 && j + 1 < a.J) load_state(hend, b * a.J + j + 1);
-    else load_state(nullptr, 0);
+    clear_state();
+    if (FULL && dir == 0 && j > 0) load_state(S, hend, static_cast<int64_t>(b) * J + j - 1);
+    if (FULL && dir == 1 && j + 1 < J) load_state(S, hend, static_cast<int64_t>(b) * J + j + 1);
     double ldec = 0.0;
     bool restarts = false;
 
-    const E *Xg = static_cast<const E *>(dir ? a.dy : a.u), *Yg = static_cast<const E *>(dir ? a.u : a.dy);
-    const E *Kg = static_cast<const E *>(dir ? a.C : a.B), *Rg = static_cast<const E *>(dir ? a.B : a.C);
-    const int64_t xb = dir ? a.dy_b : a.u_b, xt = dir ? a.dy_t : a.u_t;
-    const int64_t yb = dir ? a.u_b : a.dy_b, yt = dir ? a.u_t : a.dy_t;
-    const int64_t kb = dir ? a.C_b : a.B_b, kt = dir ? a.C_t : a.B_t;
-    const int64_t rb = dir ? a.B_b : a.C_b, rt = dir ? a.B_t : a.C_t;
-    // vecs: bits 0 B, 1 C, 2 u, 3 dy
-    const bool vk = vecs & (dir ? 2 : 1), vr = vecs & (dir ? 1 : 2);
-    const bool vx = vecs & (dir ? 8 : 4), vy = vecs & (dir ? 4 : 8);
-    auto stage_own = [&](E *dst, const E *src, int64_t stride, int n, bool vec) {
-        if (vec) {
-            constexpr int V = Seg<IO>::VW, pieces = 16 / V;
-            using Vec = typename Seg<IO>::V;
-            for (int i = lane; i < Q * pieces; i += 64) {
-                const int t = i / pieces, c = (i % pieces) * V;
-                Vec v{};
-                if (t < n && c < cols) v = *reinterpret_cast<const Vec *>(src + t * stride + c);
-                *reinterpret_cast<Vec *>(dst + t * LU + c) = v;
-            }
-        } else {
-            for (int i = lane; i < Q * 16; i += 64) {
-                const int t = i >> 4, c = i & 15;
-                dst[t * LU + c] = t < n && c < cols ? src[t * stride + c] : E(0);
-            }
+    const int64_t xt = dir ? a.dy_t : a.u_t, yt = dir ? a.u_t : a.dy_t;
+    const int64_t kt = dir ? a.C_t : a.B_t, rt = dir ? a.B_t : a.C_t;
+    const E *Xp = static_cast<const E *>(dir ? a.dy : a.u) + b * (dir ? a.dy_b : a.u_b) + gr * hpg * P;
+    const E *Yp = static_cast<const E *>(dir ? a.u : a.dy) + b * (dir ? a.u_b : a.dy_b) + gr * hpg * P;
+    const E *Kp = static_cast<const E *>(dir ? a.C : a.B) + b * (dir ? a.C_b : a.B_b) + gr * N;
+    const E *Rp = static_cast<const E *>(dir ? a.B : a.C) + b * (dir ? a.B_b : a.C_b) + gr * N;
+    const E *Tp = static_cast<const E *>(a.delta) + b * a.dt_b + h;
+
+    // the chunk on its way in registers, as in the forward walk.  Channels of
+    // a slice past the group's: past every range
+    u4 Kr[NB], Rr[FULL ? NB : 1], Xr[NU], Yr[FULL ? NU : 1];
+    uint32_t ko = 0, ro = 0, xo = 0, yo = 0;
+    float dtr = 0.0f;
+    auto channel = [&](int c) {                 // of the group; column c of 64; -1: none
+        const int i = is0 + (c >> 4), p = i % sph * 16 + (c & 15);
+        return i < hpg * sph && p < P ? i / sph * P + p : -1;
+    };
+    if constexpr (WIDE) {
+        const int t = tid / PB, c = tid % PB * V, tu = tid / PU, ch = channel(tid % PU * V);
+        ko = c < N ? static_cast<uint32_t>(t * static_cast<int>(kt) + c) * ES : kDrop;
+        ro = c < N ? static_cast<uint32_t>(t * static_cast<int>(rt) + c) * ES : kDrop;
+        xo = ch >= 0 ? static_cast<uint32_t>(tu * static_cast<int>(xt) + ch) * ES : kDrop;
+        yo = ch >= 0 ? static_cast<uint32_t>(tu * static_cast<int>(yt) + ch) * ES : kDrop;
+    }
+    auto rows = [&](u4 *r, int n, int each, const E *from, int nt, uint32_t off, int t, int64_t stride) {
+        const Rsrc v = view(from, 0x7fffffff);
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(v, t + i * each < nt ? off : kDrop,
+                                                         i * each * static_cast<int>(stride) * ES, 0);
+    };
+    auto fetch_ry = [&](const Chunk &k) {
+        if constexpr (FULL) {
+            rows(Rr, NB, 256 / PB, Rp + k.t * rt, k.n, ro, tid / PB, rt);
+            rows(Yr, NU, 256 / PU, Yp + k.t * yt, k.n, yo, tid / PU, yt);
+        }
+    };
+    auto fetch_kx = [&](const Chunk &k) {
+        rows(Kr, NB, 256 / PB, Kp + k.t * kt, k.n, ko, tid / PB, kt);
+        rows(Xr, NU, 256 / PU, Xp + k.t * xt, k.n, xo, tid / PU, xt);
+        dtr = 0.0f;
+        if (lane < k.n) {
+            const float v = IO::load(Tp + (k.t + lane) * a.dt_t, 0) + bias;
+            dtr = a.softplus ? softplus_exact(v) : v;
+        }
+    };
+    auto put_ry = [&]() {
+        if constexpr (FULL) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                M::put_perm(mem.R + (tid / PB + i * (256 / PB)) * LB, tid % PB * V, Rr[i]);
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+                *reinterpret_cast<u4 *>(mem.Y + (tid / PU + i * (256 / PU)) * LU + tid % PU * V) = Yr[i];
+        }
+    };
+    auto plain = [&](E *to, int ld, const E *from, int64_t stride, int n, bool perm) {
+        for (int i = tid; i < Q * NP; i += 256) {
+            const int t = i / NP, c = i % NP;
+            to[t * ld + (perm ? M::pos(c) : c)] = t < n && c < N ? from[t * stride + c] : E(0);
+        }
+    };
+    auto plain_ch = [&](E *to, const E *from, int64_t stride, int n) {
+        for (int i = tid; i < Q * 64; i += 256) {
+            const int t = i >> 6, c = i & 63, ch = channel(c);
+            to[t * LU + c] = t < n && ch >= 0 ? from[t * stride + ch] : E(0);
         }
     };
 
-    const int64_t c0 = j * a.Kc, c1 = c0 + a.Kc < a.nc ? c0 + a.Kc : a.nc;
-    for (int64_t x = c0; x < c1; ++x) {
-        const int64_t c = dir ? c0 + c1 - 1 - x : x;
-        const Chunk k = chunk_at(a, b, c);
-        if (k.n <= 0) continue;
-        if (dir ? k.last : k.first) {
-            load_state(dir ? a.dlast : a.h0, k.row);
+    const int c0 = j * static_cast<int>(a.Kc), c1 = min(c0 + static_cast<int>(a.Kc), static_cast<int>(a.nc));
+    auto chunk = [&](int x) {                   // the x-th of the walk, none past its end
+        Chunk k = chunk_at(a, b, dir ? c0 + c1 - 1 - x : x);
+        return k;
+    };
+    Chunk next = chunk(c0);
+    if constexpr (WIDE) {
+        fetch_ry(next);
+        fetch_kx(next);
+        put_ry();
+    }
+    for (int x = c0; x < c1; ++x) {
+        const Chunk k = next;
+        const int64_t c = row0 + (dir ? c0 + c1 - 1 - x : x);
+        if (x + 1 < c1) next = chunk(x + 1); else next.n = 0;
+        if (k.n > 0 && (dir ? k.last : k.first)) {
+            const float *from = dir ? a.dlast : a.h0;
+            if (from) load_state(S, from, k.row); else clear_state();
             restarts = true;
         }
-        stage_rows<IO, Q>(Ks, LB, Kg + k.b * kb + k.t * kt + gr * a.N, kt, k.n,
-                          static_cast<int>(a.N), NP, vk);
-        stage_own(Xs + wv * 16, Xg + k.b * xb + k.t * xt + h * a.P + p0, xt, k.n, vx);
-        if constexpr (FULL) {
-            stage_rows<IO, Q>(Rs, LB, Rg + k.b * rb + k.t * rt + gr * a.N, rt, k.n,
-                              static_cast<int>(a.N), NP, vr);
-            stage_own(Ys + wv * 16, Yg + k.b * yb + k.t * yt + h * a.P + p0, yt, k.n, vy);
+        float dt;
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                *reinterpret_cast<u4 *>(mem.K + (tid / PB + i * (256 / PB)) * LB + tid % PB * V) = Kr[i];
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+                *reinterpret_cast<u4 *>(mem.X + (tid / PU + i * (256 / PU)) * LU + tid % PU * V) = Xr[i];
+            dt = dtr;
+            fetch_ry(next);
+        } else {
+            plain(mem.K, LB, Kp + k.t * kt, kt, k.n, false);
+            plain_ch(mem.X, Xp + k.t * xt, xt, k.n);
+            if constexpr (FULL) {
+                plain(mem.R, LB, Rp + k.t * rt, rt, k.n, true);
+                plain_ch(mem.Y, Yp + k.t * yt, yt, k.n);
+            }
+            dt = 0.0f;
+            if (lane < k.n) {
+                const float v = IO::load(Tp + (k.t + lane) * a.dt_t, 0) + bias;
+                dt = a.softplus ? softplus_exact(v) : v;
+            }
         }
-        const float dt = lane < Q ? step_size<IO>(a, k, lane, h) : 0.0f;
-        const double s = lane_prefix(static_cast<double>(dt) * A2);
-        const double sQ = __shfl(s, 63, 64);
+        const double s = lane_prefix(dt * A2);
+        const double sQ = lane_value(s, 63);
         const float dec = exp2_d(sQ);
         ldec += sQ;
-        if (FULL && !idle && k.first) {
-            // the product with the start state, where there is one
-            if (sizeof(E) == 2 && dir == 1 && a.h0) {
-                float v = 0.0f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int n = 16 * nt + 4 * g + i;
-                        if (n < a.N && l < cols)
-                            v = __builtin_fmaf(S[nt][i],
-                                               a.h0[((k.row * a.H + h) * a.P + p0 + l) * a.N + n], v);
-                    }
-#pragma unroll
-                for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-                if (lane == 0) a.hdot[k.row * slices + slice] = v;
-            }
-        } else if (FULL && sizeof(E) == 2 && !idle && c % kAnchor == 0 && dec >= kDirect) {
-            f4 *to = reinterpret_cast<f4 *>(a.anchor) +
-                     (((dir * a.batch + b) * a.na + c / kAnchor) * slices + slice) * NT * 64 + lane;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) to[nt * 64] = S[nt];
-        }
-        if (FULL && sizeof(E) == 2 && dir == 0 && !idle && p0 == 0 && lane == 0)
-            a.through[(b * a.nc + c) * a.H + h] = dec;
-        if (lane < Q) {
-            const float up = exp2_d(s), down = exp2_d(sQ - s);
-            // behind the chunk's end the staged rows are zero, whatever the weight
-            ws[lane] = dir ? up : dt * down;
-            es[lane] = dir ? down : up;
-        }
+        // behind the chunk's end the staged rows are zero, whatever the weight
+        const float up = exp2_d(s), down = exp2_d(sQ - s);
+        if (lane < Q) ws[lane] = dir ? up : dt * down;
+        const float ts = dir ? dt * down : up;  // a token's share in r, p
         __syncthreads();
-        if constexpr (FULL) {
-            // ---- leave the state, and dot it with the other side's tokens
-            E *to = static_cast<E *>(dir ? a.gout : a.hin) +
-                    (((b * a.nc + c) * a.H + h) * Pr + p0 + l) * NP;
+        if (FULL && k.n > 0) {
+            // ---- leave the state: a lane's values side by side
+            E *to = static_cast<E *>(dir ? a.gout : a.hin) + ((c * slices + slice) * NT * 64 + lane) * 4;
             if (!idle) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (sizeof(E) == 2)
-                        *reinterpret_cast<uint2 *>(to + 16 * nt + 4 * g) =
-                            make_uint2(Seg<BF16>::pk(S[nt].x, S[nt].y), Seg<BF16>::pk(S[nt].z, S[nt].w));
-                    else
-                        *reinterpret_cast<f4 *>(to + 16 * nt + 4 * g) = S[nt];
+                for (int nt = 0; nt < NT; ++nt)
+                    *reinterpret_cast<typename M::Half *>(to + nt * 256) = M::half(S[nt]);
+                if (sizeof(E) == 2 && k.first) {
+                    // X of a first chunk needs the product with the start state
+                    if (dir == 1 && a.h0) {
+                        f4 h0[NT];
+                        load_state(h0, a.h0, k.row);
+                        float v = 0.0f;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const f4 q = S[nt] * h0[nt];
+                            v += (q.x + q.y) + (q.z + q.w);
+                        }
+#pragma unroll
+                        for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+                        if (lane == 0) a.hdot[k.row * slices + slice] = v;
+                    }
+                } else if (sizeof(E) == 2 && (c - row0) % kAnchor == 0 && dec >= kDirect) {
+                    f4 *an = reinterpret_cast<f4 *>(a.anchor) +
+                             (((dir * a.batch + b) * a.na + (c - row0) / kAnchor) * slices + slice) * NT * 64 + lane;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) an[nt * 64] = S[nt];
                 }
+                if (sizeof(E) == 2 && dir == 0 && p0 == 0 && lane == 0) a.through[c * H + h] = dec;
             }
+            // ---- and dot it with the other side's tokens
             f4 Y[TT];
 #pragma unroll
             for (int q = 0; q < TT; ++q) Y[q] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -199,48 +305,54 @@ __global__ __launch_bounds__(256) void heads_walk_kernel(HeadsArgs a, int vecs) 
             for (int m = 0; m < KN; ++m) {
                 const f4 x0 = S[2 * m], x1 = S[2 * m + 1];
                 float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                Frag hf[M::kTerms];
+                Frag hf[M::kTerms], rf[TT];
+#pragma unroll
+                for (int q = 0; q < TT; ++q) rf[q] = M::row_perm(mem.R + (16 * q + l) * LB + 32 * m, g);
 #pragma unroll
                 for (int z = 0; z < M::kTerms; ++z) hf[z] = M::take(v);
 #pragma unroll
-                for (int q = 0; q < TT; ++q) {
-                    const Frag rf = row_nat<IO>(Rs + (16 * q + l) * LB + 32 * m, g);
+                for (int z = 0; z < M::kTerms; ++z)
 #pragma unroll
-                    for (int z = 0; z < M::kTerms; ++z) Y[q] = M::mma(rf, hf[z], Y[q]);
-                }
+                    for (int q = 0; q < TT; ++q) Y[q] = M::mma(rf[q], hf[z], Y[q]);
             }
             float total = 0.0f;
-            float *rp = a.rp + ((dir * chunks + b * a.nc + c) * slices + slice) * Q;
+            float *rp = a.rp + ((dir * chunks + c) * slices + slice) * Q;
 #pragma unroll
-            for (int q = 0; q < TT; ++q) {
-                const f4 e = *reinterpret_cast<const f4 *>(es + 16 * q + 4 * g);
-                f4 d;
+            for (int m = 0; m < KS; ++m) {
+                float y[8];     // the operand's values are where the result's are
+                M::unpack(M::col_perm(mem.Y + 32 * m * LU + 16 * wv, LU, g, l), y);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = Y[q][i] * IO::load(Ys, (16 * q + 4 * g + i) * LU + wv * 16 + l);
+                for (int e = 0; e < 2; ++e) {
+                    const int q = 2 * m + e;
+                    f4 d;
 #pragma unroll
-                    for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
-                    d[i] = v * e[i];
-                }
-                if (l == 0 && !idle) *reinterpret_cast<f4 *>(rp + 16 * q + 4 * g) = d;
-                if (dir == 0) total += (d.x + d.y) + (d.z + d.w);
-                else {      // p_s has dt_s in it; the dot product is kept without
+                    for (int i = 0; i < 4; ++i) d[i] = row_sum(Y[q][i] * y[4 * e + i]);
+                    // kept without the decay (and dt) to the chunk's end
+                    if (l == 0 && !idle) *reinterpret_cast<f4 *>(rp + 16 * q + 4 * g) = d;
+                    if (sizeof(E) == 4) continue;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        total += d[i] * __shfl(dt, 16 * q + 4 * g + i, 64);
+                    for (int i = 0; i < 4; ++i) d[i] *= __shfl(ts, 16 * q + 4 * g + i, 64);
+                    total += (d.x + d.y) + (d.z + d.w);
                 }
             }
-            total += __shfl_xor(total, 16, 64);
-            total += __shfl_xor(total, 32, 64);
-            if (lane == 0 && !idle) a.rpsum[(dir * chunks + b * a.nc + c) * slices + slice] = total;
+            if constexpr (sizeof(E) == 2) {
+                total += __shfl_xor(total, 16, 64);
+                total += __shfl_xor(total, 32, 64);
+                if (lane == 0 && !idle) a.rpsum[(dir * chunks + c) * slices + slice] = total;
+            }
         }
+        if constexpr (FULL && WIDE) {
+            __syncthreads();
+            put_ry();
+        }
+        if constexpr (WIDE) fetch_kx(next);
         // ---- the chunk's tokens join
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) S[nt] *= dec;
 #pragma unroll
         for (int m = 0; m < KS; ++m) {
             float v[8];
-            M::unpack(M::col_perm(Xs + 32 * m * LU + wv * 16, LU, g, l), v);
+            M::unpack(M::col_perm(mem.X + 32 * m * LU + wv * 16, LU, g, l), v);
             const f4 w0 = *reinterpret_cast<const f4 *>(ws + 32 * m + 4 * g);
             const f4 w1 = *reinterpret_cast<const f4 *>(ws + 32 * m + 16 + 4 * g);
 #pragma unroll
@@ -248,20 +360,27 @@ __global__ __launch_bounds__(256) void heads_walk_kernel(HeadsArgs a, int vecs) 
             Frag wf[M::kTerms];
 #pragma unroll
             for (int z = 0; z < M::kTerms; ++z) wf[z] = M::take(v);
+            constexpr int STEP = NT < 4 ? NT : 4;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const Frag kf = M::col_perm(Ks + 32 * m * LB + 16 * nt, LB, g, l);
+            for (int n0 = 0; n0 < NT; n0 += STEP) {
+                Frag kf[STEP];
 #pragma unroll
-                for (int z = 0; z < M::kTerms; ++z) S[nt] = M::mma(kf, wf[z], S[nt]);
+                for (int i = 0; i < STEP; ++i)
+                    kf[i] = M::col_perm(mem.K + 32 * m * LB + 16 * (n0 + i), LB, g, l);
+#pragma unroll
+                for (int z = 0; z < M::kTerms; ++z)
+#pragma unroll
+                    for (int i = 0; i < STEP; ++i) S[n0 + i] = M::mma(kf[i], wf[z], S[n0 + i]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (FULL && dir == 1 && k.first && a.dh0) store_state(a.dh0, k.row);
+        if (FULL && dir == 1 && k.n > 0 && k.first && a.dh0) store_state(a.dh0, k.row);
         __syncthreads();
     }
     if constexpr (!FULL) {
-        store_state(hend, b * a.J + j);
+        store_state(hend, static_cast<int64_t>(b) * J + j);
         if (!idle && p0 == 0 && lane == 0)
-            ldecs[(b * a.J + j) * a.H + h] = restarts ? -INFINITY : static_cast<float>(ldec);
+            ldecs[(static_cast<int64_t>(b) * J + j) * H + h] = restarts ? -INFINITY : static_cast<float>(ldec);
     }
 }
 
@@ -338,384 +457,400 @@ __global__ __launch_bounds__(64) void heads_through_kernel(HeadsArgs a) {
 }
 
 // -------------------------------------------------------------- a chunk alone
+// LDS: 78 KB at 128 states in bfloat16, two workgroups a compute unit.  C is
+// needed before the heads and after them: h has its place meanwhile.  All
+// rows are kept in the permuted order.
 template <class IO, int NP, int Q, int PS>
-__global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int vecs) {
+struct ChunkMem {
+    using M = Mat<IO>;
+    using E = typename M::E;
+    static constexpr int LB = NP + (sizeof(E) == 2 ? 16 : M::kPad), LU = PS + M::kPad;
+    static constexpr int LW = Q + M::kPad, TT = Q / 16, TRI = TT * (TT + 1) / 2;
+    static constexpr int kC = (Q > PS ? Q : PS) * LB;
+    __attribute__((aligned(16))) E B[Q * LB];
+    __attribute__((aligned(16))) E HC[kC];                      // h_in; C
+    __attribute__((aligned(16))) E G[PS * LB > Q * LW ? PS * LB : Q * LW];     // gh; at last W
+    __attribute__((aligned(16))) E U[Q * LU];
+    __attribute__((aligned(16))) E Y[Q * LU];
+    __attribute__((aligned(16))) typename M::Half Mh[TRI * 64];
+    // a head's tokens: exp(s), exp(s_Q - s), exp(s - r), s - r and dt with r the
+    // sum before the token's tile; exp(r_q - s) for the tiles q behind it
+    __attribute__((aligned(16))) float tok[5 * Q + TT * (TT - 1) / 2 * 16];
+};
+
+// What a chunk and head leave for heads_grad_kernel: row and column sums of Z
+// by tiles (the columns' without dt), dy_t.u_t and Z_tt, and <gh, h_in>.
+template <int Q>
+struct GradRec {
+    static constexpr int TT = Q / 16, TRI = TT * (TT + 1) / 2;
+    float rowz[TRI * 16], colv[TRI * 16], diag[Q], diagz[Q], xdot[4];
+};
+
+// Which tiles (q, r) of a triangle wavefront w has, o = 0, 1, ...; r < 0: none.
+template <int TT>
+__device__ __forceinline__ constexpr int own_q(int w, int o) {
+    if constexpr (TT == 2) return w == 0 ? 0 : 1;
+    return w == 3 ? (o == 0 ? 0 : 3) : 3 - w;
+}
+template <int TT>
+__device__ __forceinline__ constexpr int own_r(int w, int o) {
+    if constexpr (TT == 2) return o == 0 && w < 3 ? (w == 2 ? 1 : 0) : -1;
+    return w == 3 ? (o == 0 ? 0 : o == 1 ? 3 : -1) : o <= (w == 2 ? 1 : 2) ? o : -1;
+}
+
+template <class IO, int NP, int Q, int PS, bool WIDE>
+__global__ __launch_bounds__(256, (sizeof(ChunkMem<IO, NP, Q, PS>) <= 80 * 1024 ? 2 : 1)) void
+heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     using M = Mat<IO>;
     using E = typename M::E;
     using Frag = typename M::Frag;
+    using Half = typename M::Half;
+    using Mem = ChunkMem<IO, NP, Q, PS>;
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    constexpr int V = Seg<IO>::VW, ES = sizeof(E);
     constexpr int NT = NP / 16, KN = NP / 32, TT = Q / 16, KS = Q / 32, KP = PS / 32;
-    constexpr int LB = NP + M::kPad, LU = PS + M::kPad, LW = Q + M::kPad;
-    constexpr int TRI = TT * (TT + 1) / 2, OWN = (TRI + 3) / 4, NW = (NT + 3) / 4;
-    constexpr int SB = Q * LB, SU = Q * LU, SH = PS * LB;
-    extern __shared__ __attribute__((aligned(16))) unsigned char mem[];
-    E *Bs = reinterpret_cast<E *>(mem), *Cs = Bs + SB, *Us = Cs + SB, *Ys = Us + SU,
-      *Hs = Ys + SU, *Gs = Hs + SH, *Mf = Gs + SH;      // Mf: TRI x 64 lanes x 4
-    f4 *CB = reinterpret_cast<f4 *>(Mf + TRI * 256);    // rows t, columns s
-    float *tok = reinterpret_cast<float *>(CB + TRI * 64);
-    float *es = tok, *we = tok + Q, *rt = tok + 2 * Q, *sd = tok + 3 * Q, *dts = tok + 4 * Q,
-          *cx = tok + 5 * Q;                            // cx: TT - 1 rows
-    float *colv = tok + (4 + TT) * Q;                   // TRI x 16 each
-    float *rowz = colv + TRI * 16, *diag = rowz + TRI * 16, *diagz = diag + Q;   // Q each
-    float *through = diagz + Q;                         // one a wavefront
-    E *Ws = Hs;                                         // at the end: Q x LW
+    constexpr int LB = Mem::LB, LU = Mem::LU, LW = Mem::LW;
+    constexpr int OWN = TT == 2 ? 1 : 3, NW = (NT + 3) / 4, FOUR = M::pos(4);
+    constexpr int PU = PS / V, NU = Q * PU / 256, NS = PS * NP / V / 256;    // pieces of u (dy), h (gh)
+    static_assert(Q * PU % 256 == 0 && PS * NP / V % 256 == 0, "whole rounds of the workgroup");
+    extern __shared__ __attribute__((aligned(16))) unsigned char raw[];
+    Mem &mem = *reinterpret_cast<Mem *>(raw);
 
-    const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-    const int64_t chunks = a.batch * a.nc, hpg = a.H / a.G;
-    const int64_t ci = blockIdx.x % chunks, rest = blockIdx.x / chunks;
-    const int64_t gr = rest % a.G, hs = rest / a.G;
+    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63, g = lane >> 4, l = lane & 15;
+    const int N = static_cast<int>(a.N), P = static_cast<int>(a.P), H = static_cast<int>(a.H);
+    const int G = static_cast<int>(a.G), hpg = H / G, sph = (P + 15) / 16;
+    const int id = static_cast<int>(by_xcd(blockIdx.x, gridDim.x));
+    const int hs = id % static_cast<int>(a.hsplit), gr = id / static_cast<int>(a.hsplit) % G;
+    const int ci = id / static_cast<int>(a.hsplit * G);
     const Chunk k = chunk_at(a, ci / a.nc, ci % a.nc);
-    const int64_t h0 = gr * hpg + hs * a.hblk;
-    const int64_t h1 = (hs + 1) * a.hblk < hpg ? h0 + a.hblk : (gr + 1) * hpg;
-    if (k.n <= 0) {         // an unused chunk of a packed batch: nothing to add
-        if (static_cast<int64_t>(threadIdx.x) < h1 - h0)
-            for (int64_t h = h0 + threadIdx.x; h < h1; h += 256)
-                for (int i = 0; i < 3; ++i) a.part[(i * chunks + ci) * a.H + h] = 0.0f;
-        return;
-    }
-    const int64_t sph = (a.P + 15) / 16, Pr = sph * 16, slices = a.H * sph;
+    if (k.n <= 0) return;           // an unused chunk of a packed batch
+    const int h0 = gr * hpg + hs * static_cast<int>(a.hblk);
+    const int h1 = min(h0 + static_cast<int>(a.hblk), (gr + 1) * hpg);
+    const int slices = H * sph;
 
-    stage_rows<IO, Q>(Bs, LB, static_cast<const E *>(a.B) + k.b * a.B_b + k.t * a.B_t + gr * a.N,
-                      a.B_t, k.n, static_cast<int>(a.N), NP, vecs & 1);
-    stage_rows<IO, Q>(Cs, LB, static_cast<const E *>(a.C) + k.b * a.C_b + k.t * a.C_t + gr * a.N,
-                      a.C_t, k.n, static_cast<int>(a.N), NP, vecs & 2);
-    __syncthreads();
-    {   // C_t . B_s once for all heads
-        int id = 0;
-#pragma unroll
-        for (int q = 0; q < TT; ++q)
-#pragma unroll
-            for (int r = 0; r <= q; ++r, ++id)
-                if ((id & 3) == wv) {
-                    f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int m = 0; m < KN; ++m)
-                        acc = M::mma(M::row(Cs + (16 * q + l) * LB + 32 * m, g),
-                                     M::row(Bs + (16 * r + l) * LB + 32 * m, g), acc);
-                    CB[id * 64 + lane] = acc;
-                }
+    const E *Bp = static_cast<const E *>(a.B) + k.b * a.B_b + k.t * a.B_t + gr * N;
+    const E *Cp = static_cast<const E *>(a.C) + k.b * a.C_b + k.t * a.C_t + gr * N;
+    const E *Up = static_cast<const E *>(a.u) + k.b * a.u_b + k.t * a.u_t;
+    const E *Yp = static_cast<const E *>(a.dy) + k.b * a.dy_b + k.t * a.dy_t;
+    const E *Tp = static_cast<const E *>(a.delta) + k.b * a.dt_b + k.t * a.dt_t;
+    E *Dp = static_cast<E *>(a.du) + (k.b * a.L + k.t) * a.H * a.P;
+
+    auto put_bc = [&](E *to, const E *from, int64_t stride) {
+        if constexpr (WIDE) {
+            for (int i = tid; i < Q * NP / V; i += 256) {
+                const int t = i / (NP / V), c = i % (NP / V) * V;
+                u4 v = {0, 0, 0, 0};
+                if (t < k.n && c < N) v = *reinterpret_cast<const u4 *>(from + t * stride + c);
+                M::put_perm(to + t * LB, c, v);
+            }
+        } else {
+            for (int i = tid; i < Q * NP; i += 256) {
+                const int t = i / NP, c = i % NP;
+                to[t * LB + M::pos(c)] = t < k.n && c < N ? from[t * stride + c] : E(0);
+            }
+        }
+    };
+
+    // ---- the next head's tokens and states on their way in registers
+    u4 Ur[NU], Yr[NU], Hr[NS], Gr[NS];
+    uint32_t uo = 0, yo = 0;
+    float dtr = 0.0f;
+    if constexpr (WIDE) {
+        const int t = tid / PU, c = tid % PU * V;
+        uo = static_cast<uint32_t>(t * static_cast<int>(a.u_t) + c) * ES;
+        yo = static_cast<uint32_t>(t * static_cast<int>(a.dy_t) + c) * ES;
     }
-    f4 dB[TT][NW], dC[TT][NW], W[OWN];
+    auto fetch = [&](int h, int p0) {
+        if constexpr (WIDE) {
+            const Rsrc ru = view(Up + h * P + p0, 0x7fffffff), ry = view(Yp + h * P + p0, 0x7fffffff);
+            const bool in = p0 + tid % PU * V < P;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                const bool ok = in && tid / PU + i * (256 / PU) < k.n;
+                Ur[i] = __builtin_amdgcn_raw_buffer_load_b128(ru, ok ? uo : kDrop,
+                                                              i * (256 / PU) * static_cast<int>(a.u_t) * ES, 0);
+                Yr[i] = __builtin_amdgcn_raw_buffer_load_b128(ry, ok ? yo : kDrop,
+                                                              i * (256 / PU) * static_cast<int>(a.dy_t) * ES, 0);
+            }
+        }
+        dtr = 0.0f;
+        if (lane < k.n) {
+            const float v = IO::load(Tp + lane * a.dt_t, h) + (a.bias ? a.bias[h] : 0.0f);
+            dtr = a.softplus ? softplus_exact(v) : v;
+        }
+    };
+    auto fetch_states = [&](int h, int p0) {
+        // states: 16 channels behind one another, nothing past the head's last
+        const int64_t at = (static_cast<int64_t>(ci) * slices + h * sph + p0 / 16) * NT * 256;
+        const uint32_t bytes = static_cast<uint32_t>(min(PS / 16, sph - p0 / 16)) * NT * 256 * ES;
+        const Rsrc rh = view(static_cast<const E *>(a.hin) + at, bytes);
+        const Rsrc rg = view(static_cast<const E *>(a.gout) + at, bytes);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            Hr[i] = __builtin_amdgcn_raw_buffer_load_b128(rh, (tid + 256 * i) * 16, 0, 0);
+            Gr[i] = __builtin_amdgcn_raw_buffer_load_b128(rg, (tid + 256 * i) * 16, 0, 0);
+        }
+    };
+    // a piece of a state, as the walks' lanes left it, into rows of channels
+    auto put_state = [&](E *to, int x, const u4 &v) {
+        constexpr int LN = V / 4;               // lanes a piece
+        const int sl = x / (NT * 64 / LN), nt = x / (64 / LN) % NT, ln = x % (64 / LN) * LN;
+        E *at = to + (16 * sl + (ln & 15)) * LB + M::pos(16 * nt + 4 * (ln >> 4));
+        Half hv[LN];
+        __builtin_memcpy(hv, &v, 16);
+#pragma unroll
+        for (int i = 0; i < LN; ++i) *reinterpret_cast<Half *>(at + i * LB) = hv[i];
+    };
+
+    put_bc(mem.B, Bp, a.B_t);
+    put_bc(mem.HC, Cp, a.C_t);
+    fetch(h0, 0);
+    fetch_states(h0, 0);
+    __syncthreads();
+    f4 CB[OWN], W[OWN], DX[OWN], dB[TT][NW], dC[TT][NW];
+    const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {             // C_t . B_s: rows t, columns s
+        W[o] = CB[o] = DX[o] = zero;
+        const int r = own_r<TT>(wv, o), q = own_q<TT>(wv, o);
+        if (r >= 0)
+#pragma unroll
+            for (int m = 0; m < KN; ++m)
+                CB[o] = M::mma(M::row_perm(mem.HC + (16 * q + l) * LB + 32 * m, g),
+                               M::row_perm(mem.B + (16 * r + l) * LB + 32 * m, g), CB[o]);
+    }
 #pragma unroll
     for (int q = 0; q < TT; ++q)
 #pragma unroll
-        for (int n = 0; n < NW; ++n) dB[q][n] = dC[q][n] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int o = 0; o < OWN; ++o) W[o] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < NW; ++n) dB[q][n] = dC[q][n] = zero;
+    __syncthreads();                            // C gives its place to h
 
-    for (int64_t h = h0; h < h1; ++h) {
-        const float A2 = a.A[h] * kLog2e, Dh = a.D ? a.D[h] : 0.0f;
-        const float dt = lane < Q ? step_size<IO>(a, k, lane, h) : 0.0f;
-        const double s = lane_prefix(static_cast<double>(dt) * A2);
-        const double sQ = __shfl(s, 63, 64);
-        __syncthreads();    // the head before is done with tok and Mf
-        if (wv == 0) {
+    float *es = mem.tok, *we = es + Q, *rt = es + 2 * Q, *sd = es + 3 * Q, *dts = es + 4 * Q, *cx = es + 5 * Q;
+    float xdot = 0.0f;
+    int h = h0, p0 = 0;
+    while (h < h1) {
+        const double A2 = static_cast<double>(a.A[h]) * 1.4426950408889634;
+        const float Dh = a.D ? a.D[h] : 0.0f;
+        // ---- stage
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                M::put_perm(mem.U + (tid / PU + i * (256 / PU)) * LU, tid % PU * V, Ur[i]);
+                M::put_perm(mem.Y + (tid / PU + i * (256 / PU)) * LU, tid % PU * V, Yr[i]);
+            }
+        } else {
+            for (int i = tid; i < Q * PS; i += 256) {
+                const int t = i / PS, c = i % PS;
+                const bool in = t < k.n && p0 + c < P;
+                mem.U[t * LU + M::pos(c)] = in ? Up[t * a.u_t + h * P + p0 + c] : E(0);
+                mem.Y[t * LU + M::pos(c)] = in ? Yp[t * a.dy_t + h * P + p0 + c] : E(0);
+            }
+        }
+        const float dt = dtr;
+        const double s = lane_prefix(dt * A2);
+        const double sQ = lane_value(s, 63);
+        // X from the staged states themselves: exact in float32; in bfloat16 its
+        // error, 2^-9 of X, is the smaller one where the chunk keeps little
+        const bool direct = ES == 4 || exp2_d(sQ) < kDirect;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            put_state(mem.HC, tid + 256 * i, Hr[i]);
+            put_state(mem.G, tid + 256 * i, Gr[i]);
+            if (direct) {
+                float x[V], y[V];
+                typename Seg<IO>::V hv, gv;
+                __builtin_memcpy(&hv, &Hr[i], 16);
+                __builtin_memcpy(&gv, &Gr[i], 16);
+                Seg<IO>::unpack(hv, x);
+                Seg<IO>::unpack(gv, y);
+#pragma unroll
+                for (int e = 0; e < V; ++e) xdot = __builtin_fmaf(x[e], y[e], xdot);
+            }
+        }
+        const int hn = p0 + PS < P ? h : h + 1, pn = p0 + PS < P ? p0 + PS : 0;
+        const bool last = hn != h;
+        if (hn < h1) fetch(hn, pn);
+        if (p0 == 0 && lane < Q) {
             double ref[TT];
             ref[0] = 0.0;
 #pragma unroll
-            for (int q = 1; q < TT; ++q) ref[q] = __shfl(s, 16 * q - 1, 64);
-            double own = 0.0;
+            for (int q = 1; q < TT; ++q) ref[q] = lane_value(s, 16 * q - 1);
+            if (wv == 0) es[lane] = exp2_d(s);
+            if (wv == 1) { we[lane] = exp2_d(sQ - s); dts[lane] = dt; }
+            if (wv == 2) {
+                double own = 0.0;
 #pragma unroll
-            for (int q = 1; q < TT; ++q) own = (lane >> 4) == q ? ref[q] : own;
-            if (lane < Q) {
-                es[lane] = exp2_d(s);
-                we[lane] = exp2_d(sQ - s);
+                for (int q = 1; q < TT; ++q) own = g == q ? ref[q] : own;
                 rt[lane] = exp2_d(s - own);
                 sd[lane] = static_cast<float>(s - own);
-                dts[lane] = dt;
+            }
+            if (wv == 3) {
 #pragma unroll
                 for (int q = 1; q < TT; ++q)
-                    cx[(q - 1) * Q + lane] = lane < 16 * q ? exp2_d(ref[q] - s) : 0.0f;
+                    if (g < q) cx[q * (q - 1) / 2 * 16 + lane] = exp2_d(ref[q] - s);
             }
         }
-        // X from the staged states themselves: exact in float32; in bfloat16 its
-        // error, 2^-9 of X, is the smaller one where the chunk keeps little
-        const bool direct = sizeof(E) == 4 || exp2_d(sQ) < kDirect;
-        float xdot = 0.0f;
-        f4 DX[OWN];
-#pragma unroll
-        for (int o = 0; o < OWN; ++o) DX[o] = f4{0.0f, 0.0f, 0.0f, 0.0f};
         __syncthreads();
-        // decay of tile (q, r) in this lane: rows t = 4g + i, column s = l
-        auto decay = [&](int q, int r) {
-            f4 v;
+        // ---- the wavefront's tiles: decayed products for v (k = t), dy_t . u_s
+        GradRec<Q> *rc = rec + static_cast<int64_t>(ci) * H + h;
+        if (p0 == 0) {
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) DX[o] = zero;
+        }
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            const int r = own_r<TT>(wv, o), q = own_q<TT>(wv, o), idx = q * (q + 1) / 2 + r;
+            if (r < 0) continue;
+#pragma unroll
+            for (int m = 0; m < KP; ++m)
+                DX[o] = M::mma(M::row_perm(mem.Y + (16 * q + l) * LU + 32 * m, g),
+                               M::row_perm(mem.U + (16 * r + l) * LU + 32 * m, g), DX[o]);
+            if (p0 != 0 && !last) continue;
+            // decay from s (column l) to t (rows 4g + i)
+            f4 d;
             if (r < q) {
-                const float c = cx[(q - 1) * Q + 16 * r + l];
-                v = *reinterpret_cast<const f4 *>(rt + 16 * q + 4 * g) * c;
+                d = *reinterpret_cast<const f4 *>(rt + 16 * q + 4 * g) * cx[q * (q - 1) / 2 * 16 + 16 * r + l];
             } else {
                 const float x = sd[16 * r + l];
                 const f4 y = *reinterpret_cast<const f4 *>(sd + 16 * q + 4 * g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = l <= 4 * g + i ? exp2_hw(y[i] - x) : 0.0f;
+                for (int i = 0; i < 4; ++i) d[i] = l <= 4 * g + i ? exp2_hw(y[i] - x) : 0.0f;
             }
-            return v;
-        };
-        {   // decayed products for v, as operands with k = t
-            int id = 0;
+            if (p0 == 0) mem.Mh[idx * 64 + lane] = M::half(CB[o] * d);
+            if (last) {
+                const f4 x = DX[o] * d, z = x * CB[o];
+                const float ds = dts[16 * r + l];
+                W[o] += x * ds;
+                float col = (z.x + z.y) + (z.z + z.w);
+                col += __shfl_xor(col, 16, 64);
+                col += __shfl_xor(col, 32, 64);
+                if (g == 0) rc->colv[idx * 16 + l] = col;
+                f4 row;
 #pragma unroll
-            for (int q = 0; q < TT; ++q)
-#pragma unroll
-                for (int r = 0; r <= q; ++r, ++id)
-                    if ((id & 3) == wv) {
-                        const f4 m = CB[id * 64 + lane] * decay(q, r);
-                        if constexpr (sizeof(E) == 2)
-                            *reinterpret_cast<uint2 *>(Mf + (id * 64 + lane) * 4) =
-                                make_uint2(Seg<BF16>::pk(m.x, m.y), Seg<BF16>::pk(m.z, m.w));
-                        else
-                            *reinterpret_cast<f4 *>(Mf + (id * 64 + lane) * 4) = m;
-                    }
-        }
-        for (int p0 = 0; p0 < a.P; p0 += PS) {
-            const int pc = static_cast<int>(a.P - p0 < PS ? a.P - p0 : PS);
-            if (p0) __syncthreads();
-            stage_rows<IO, Q>(Us, LU, static_cast<const E *>(a.u) + k.b * a.u_b + k.t * a.u_t + h * a.P + p0,
-                              a.u_t, k.n, pc, PS, vecs & 4);
-            stage_rows<IO, Q>(Ys, LU, static_cast<const E *>(a.dy) + k.b * a.dy_b + k.t * a.dy_t + h * a.P + p0,
-                              a.dy_t, k.n, pc, PS, vecs & 8);
-            const int64_t so = ((ci * a.H + h) * Pr + p0) * NP;
-            const int prow = static_cast<int>(Pr - p0 < PS ? Pr - p0 : PS);
-            stage_rows<IO, PS>(Hs, LB, static_cast<const E *>(a.hin) + so, NP, prow, NP, NP, true);
-            stage_rows<IO, PS>(Gs, LB, static_cast<const E *>(a.gout) + so, NP, prow, NP, NP, true);
-            __syncthreads();
-            if (direct) {
-                constexpr int V = Seg<IO>::VW;
-                for (int i = threadIdx.x; i < PS * NP / V; i += 256) {
-                    const int at = i / (NP / V) * LB + i % (NP / V) * V;
-                    float x[V], y[V];
-                    load_vec<IO, V>(Hs + at, x);
-                    load_vec<IO, V>(Gs + at, y);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) xdot = __builtin_fmaf(x[e], y[e], xdot);
-                }
-            }
-            {   // dy_t . u_s
-                int id = 0;
-#pragma unroll
-                for (int q = 0; q < TT; ++q)
-#pragma unroll
-                    for (int r = 0; r <= q; ++r, ++id)
-                        if ((id & 3) == wv) {
-#pragma unroll
-                            for (int m = 0; m < KP; ++m)
-                                DX[id >> 2] = M::mma(M::row(Ys + (16 * q + l) * LU + 32 * m, g),
-                                                     M::row(Us + (16 * r + l) * LU + 32 * m, g),
-                                                     DX[id >> 2]);
-                        }
-            }
-            f4 V[TT];
-            if (16 * wv < PS) {     // du of 16 channels a wavefront
-                f4 I[TT];
-#pragma unroll
-                for (int r = 0; r < TT; ++r) V[r] = I[r] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int m = 0; m < KN; ++m) {
-                    const Frag gf = M::row(Gs + (16 * wv + l) * LB + 32 * m, g);
-#pragma unroll
-                    for (int r = 0; r < TT; ++r)
-                        I[r] = M::mma(M::row(Bs + (16 * r + l) * LB + 32 * m, g), gf, I[r]);
-                }
-#pragma unroll
-                for (int m = 0; m < KS; ++m) {
-                    const Frag yf = M::col_perm(Ys + 32 * m * LU + 16 * wv, LU, g, l);
-#pragma unroll
-                    for (int r = 0; r < 2 * m + 2; ++r) {
-                        float v[8];
-                        Frag mf;
-                        const int i1 = (2 * m + 1) * (2 * m + 2) / 2 + r, i0 = 2 * m * (2 * m + 1) / 2 + r;
-                        if constexpr (sizeof(E) == 2) {
-                            typename Mat<BF16>::Bits bits;
-                            bits.d[0] = r <= 2 * m ? *reinterpret_cast<const uint2 *>(Mf + (i0 * 64 + lane) * 4)
-                                                   : make_uint2(0, 0);
-                            bits.d[1] = *reinterpret_cast<const uint2 *>(Mf + (i1 * 64 + lane) * 4);
-                            mf = bits.f;
-                        } else {
-                            const f4 hi = *reinterpret_cast<const f4 *>(Mf + (i1 * 64 + lane) * 4);
-                            f4 lo = {0.0f, 0.0f, 0.0f, 0.0f};
-                            if (r <= 2 * m) lo = *reinterpret_cast<const f4 *>(Mf + (i0 * 64 + lane) * 4);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
-                            mf = M::pack(v);
-                        }
-                        V[r] = M::mma(mf, yf, V[r]);
+                for (int i = 0; i < 4; ++i) {
+                    // the diagonal crosses no decay
+                    row[i] = row_sum(r < q || l < 4 * g + i ? z[i] * ds : 0.0f);
+                    if (r == q && l == 4 * g + i) {
+                        rc->diag[16 * q + l] = DX[o][i];
+                        rc->diagz[16 * q + l] = z[i];
                     }
                 }
-#pragma unroll
-                for (int r = 0; r < TT; ++r) {
-                    const f4 w = *reinterpret_cast<const f4 *>(we + 16 * r + 4 * g);
-                    const f4 d = *reinterpret_cast<const f4 *>(dts + 16 * r + 4 * g);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        V[r][i] = d[i] * __builtin_fmaf(w[i], I[r][i], V[r][i]) +
-                                  Dh * IO::load(Ys, (16 * r + 4 * g + i) * LU + 16 * wv + l);
-                }
-            }
-            // what the states give dC and dB: a quarter of the columns n a wavefront
-#pragma unroll
-            for (int n = 0; n < NW; ++n) {
-                const int nt = wv * NW + n;
-                if (nt >= NT) break;
-                Frag hf[KP], gf[KP];
-#pragma unroll
-                for (int m = 0; m < KP; ++m) {
-                    hf[m] = M::col_perm(Hs + 32 * m * LB + 16 * nt, LB, g, l);
-                    gf[m] = M::col_perm(Gs + 32 * m * LB + 16 * nt, LB, g, l);
-                }
-#pragma unroll
-                for (int q = 0; q < TT; ++q) {
-                    f4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
-#pragma unroll
-                    for (int m = 0; m < KP; ++m) {
-                        x = M::mma(row_nat<IO>(Ys + (16 * q + l) * LU + 32 * m, g), hf[m], x);
-                        y = M::mma(row_nat<IO>(Us + (16 * q + l) * LU + 32 * m, g), gf[m], y);
-                    }
-                    const f4 e = *reinterpret_cast<const f4 *>(es + 16 * q + 4 * g);
-                    const f4 w = *reinterpret_cast<const f4 *>(we + 16 * q + 4 * g) *
-                                 *reinterpret_cast<const f4 *>(dts + 16 * q + 4 * g);
-                    dC[q][n] += e * x;
-                    dB[q][n] += w * y;
-                }
-            }
-            __syncthreads();        // u is no longer read: du goes out through its place
-            if (16 * wv < PS) {
-#pragma unroll
-                for (int r = 0; r < TT; ++r)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        IO::store(Us, (16 * r + 4 * g + i) * LU + 16 * wv + l, V[r][i]);
-            }
-            __syncthreads();
-            E *dug = static_cast<E *>(a.du) + ((k.b * a.L + k.t) * a.H + h) * a.P + p0;
-            const int64_t ds = a.H * a.P;
-            if (vecs & 16) {
-                constexpr int Vw = Seg<IO>::VW, per = PS / Vw;
-                using Vec = typename Seg<IO>::V;
-                for (int i = threadIdx.x; i < Q * per; i += 256) {
-                    const int t = i / per, c = (i % per) * Vw;
-                    if (t < k.n && c < pc)
-                        *reinterpret_cast<Vec *>(dug + t * ds + c) = *reinterpret_cast<const Vec *>(Us + t * LU + c);
-                }
-            } else {
-                for (int i = threadIdx.x; i < Q * PS; i += 256) {
-                    const int t = i / PS, c = i % PS;
-                    if (t < k.n && c < pc) dug[t * ds + c] = Us[t * LU + c];
-                }
+                if (l == 0) *reinterpret_cast<f4 *>(rc->rowz + idx * 16 + 4 * g) = row;
             }
         }
-        {   // sums of the decayed products over rows and columns, and W
-            int id = 0;
-#pragma unroll
-            for (int q = 0; q < TT; ++q)
-#pragma unroll
-                for (int r = 0; r <= q; ++r, ++id)
-                    if ((id & 3) == wv) {
-                        const f4 x = DX[id >> 2] * decay(q, r), z = x * CB[id * 64 + lane];
-                        const float ds = dts[16 * r + l];
-                        W[id >> 2] += x * ds;
-                        float col = (z.x + z.y) + (z.z + z.w);
-                        col += __shfl_xor(col, 16, 64);
-                        col += __shfl_xor(col, 32, 64);
-                        if (g == 0) colv[id * 16 + l] = col;
-                        f4 row;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // the diagonal crosses no decay
-                            float v = r < q || l < 4 * g + i ? z[i] * ds : 0.0f;
-#pragma unroll
-                            for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
-                            row[i] = v;
-                            if (r == q && l == 4 * g + i) {
-                                diag[16 * q + l] = DX[id >> 2][i];          // dy_t . u_t
-                                diagz[16 * q + l] = z[i];                   // its share of colv
-                            }
-                        }
-                        if (l == 0) *reinterpret_cast<f4 *>(rowz + id * 16 + 4 * g) = row;
-                    }
-        }
-        if (direct) {
+        if (last && direct) {
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) xdot += __shfl_xor(xdot, o, 64);
-            if (lane == 0) through[wv] = xdot;
+            if (lane == 0) rc->xdot[wv] = xdot;
         }
-        __syncthreads();
-        if (wv == 0) {      // a lane a token
-            // E without differences of long sums: of the tiles (q, r) of Z, those
-            // with r < own < q count whole, those of the own row from the token
-            // on, those of the own column up to it; only the tile on the
-            // diagonal is a difference
-            float cv = 0.0f, dd = 0.0f, r = 0.0f, p = 0.0f;
-            double rows = 0.0, cols_ = 0.0, whole = 0.0;
-            if (lane < Q) {
-                const int own = lane >> 4, dg = own * (own + 1) / 2 + own;
-                for (int q = own + 1; q < TT; ++q) {
-                    const int at = q * (q + 1) / 2;
-                    cv += colv[(at + own) * 16 + l];
-                    for (int x = 0; x < own; ++x)
-                        for (int i = 0; i < 16; i += 4) {
-                            const f4 w = *reinterpret_cast<const f4 *>(rowz + (at + x) * 16 + i);
-                            whole += (w.x + w.y) + (w.z + w.w);
-                        }
-                }
-                cols_ = static_cast<double>(cv) * dt;
-                for (int x = 0; x < own; ++x) rows += rowz[(own * (own + 1) / 2 + x) * 16 + l];
-                rows += static_cast<double>(rowz[dg * 16 + l]) -
-                        static_cast<double>(colv[dg * 16 + l] - diagz[lane]) * dt;
-                cv += colv[dg * 16 + l];
-                dd = diag[lane];
-                const float *rp = a.rp + (ci * slices + h * sph) * Q + lane;
-                for (int64_t i = 0; i < sph; ++i) {
-                    r += rp[i * Q];
-                    p += rp[chunks * slices * Q + i * Q];
-                }
+        if (last) xdot = 0.0f;
+        // ---- what the states give dC and dB: a quarter of the columns n a wavefront
+#pragma unroll
+        for (int n = 0; n < NW; ++n) {
+            const int nt = wv * NW + n;
+            if (nt >= NT) break;
+            Frag hf[KP], gf[KP];
+#pragma unroll
+            for (int m = 0; m < KP; ++m) {
+                hf[m] = M::template col_perm<8>(mem.HC + 32 * m * LB + M::pos(16 * nt), LB, g, l);
+                gf[m] = M::template col_perm<8>(mem.G + 32 * m * LB + M::pos(16 * nt), LB, g, l);
             }
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) {      // rows: from the token on; columns: up to it
-                const double x = __shfl_down(rows, o, 16), y = __shfl_up(cols_, o, 16);
-                if (l + o < 16) rows += x;
-                if (l >= o) cols_ += y;
-            }
-            const double before = __shfl_up(cols_, 1, 16);
-            const double pd = static_cast<double>(p) * dt;
-            const double rs = lane_prefix(static_cast<double>(r)), ps = lane_prefix(pd);
-            const float X = direct ? exp2_d(sQ) * ((through[0] + through[1]) + (through[2] + through[3]))
-                                   : a.through[ci * a.H + h];
-            const double E_ = X + (__shfl(rs, 63, 64) - rs + r) + (ps - pd) + whole + rows +
-                              (l ? before : 0.0);
-            const float ddt = cv + p + a.A[h] * static_cast<float>(E_);
-            float dd_ = 0.0f;
-            if (lane < k.n) {
-                float raw = IO::load(static_cast<const E *>(a.delta) + k.b * a.dt_b + (k.t + lane) * a.dt_t, h);
-                if (a.bias) raw += a.bias[h];
-                dd_ = a.softplus ? ddt / (1.0f + expf(-raw)) : ddt;
-                IO::store(static_cast<E *>(a.ddelta) + (k.b * a.L + k.t + lane) * a.H, h, dd_);
-            }
-            double sA = lane < k.n ? E_ * dt : 0.0, sD = lane < k.n ? dd : 0.0f, sb = dd_;
+            for (int q = 0; q < TT; ++q) {
+                f4 x = zero, y = zero;
 #pragma unroll
-            for (int o = 32; o > 0; o >>= 1) {
-                sA += __shfl_xor(sA, o, 64);
-                sD += __shfl_xor(sD, o, 64);
-                sb += __shfl_xor(sb, o, 64);
-            }
-            if (lane == 0) {
-                a.part[ci * a.H + h] = static_cast<float>(sA);
-                a.part[(chunks + ci) * a.H + h] = static_cast<float>(sD);
-                a.part[(2 * chunks + ci) * a.H + h] = static_cast<float>(sb);
+                for (int m = 0; m < KP; ++m) {
+                    x = M::mma(M::row_perm(mem.Y + (16 * q + l) * LU + 32 * m, g), hf[m], x);
+                    y = M::mma(M::row_perm(mem.U + (16 * q + l) * LU + 32 * m, g), gf[m], y);
+                }
+                dC[q][n] += *reinterpret_cast<const f4 *>(es + 16 * q + 4 * g) * x;
+                dB[q][n] += *reinterpret_cast<const f4 *>(we + 16 * q + 4 * g) *
+                            *reinterpret_cast<const f4 *>(dts + 16 * q + 4 * g) * y;
             }
         }
-    }
-    // ---- W over all heads, as rows t by columns s; nothing above the diagonal
-    __syncthreads();
-    for (int i = threadIdx.x; i < Q * LW; i += 256) Ws[i] = E(0);
-    __syncthreads();
-    {
-        int id = 0;
+        __builtin_amdgcn_sched_barrier(0);
+        if (hn < h1) fetch_states(hn, pn);
+        // ---- du of 16 channels a wavefront: first what gh gives
+        f4 X[TT];
+        if (16 * wv < PS) {
 #pragma unroll
-        for (int q = 0; q < TT; ++q)
+            for (int r = 0; r < TT; ++r) X[r] = zero;
 #pragma unroll
-            for (int r = 0; r <= q; ++r, ++id)
-                if ((id & 3) == wv) {
+            for (int m = 0; m < KN; ++m) {
+                const Frag gf = M::row_perm(mem.G + (16 * wv + l) * LB + 32 * m, g);
+#pragma unroll
+                for (int r = 0; r < TT; ++r)
+                    X[r] = M::mma(M::row_perm(mem.B + (16 * r + l) * LB + 32 * m, g), gf, X[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < TT; ++r) X[r] *= *reinterpret_cast<const f4 *>(we + 16 * r + 4 * g);
+        }
+        __syncthreads();                        // Mh is there; nobody reads u any more
+        if (16 * wv < PS) {
+            E *Ud = mem.U + M::pos(16 * wv) + (l >> 2) * FOUR + (l & 3);   // du in u's place
+            Frag yf[KS];
+#pragma unroll
+            for (int m = 0; m < KS; ++m) {
+                yf[m] = M::template col_perm<8>(mem.Y + 32 * m * LU + M::pos(16 * wv), LU, g, l);
+#pragma unroll
+                for (int r = 0; r < 2 * m + 2; ++r) {
+                    const int i1 = (2 * m + 1) * (2 * m + 2) / 2 + r, i0 = 2 * m * (2 * m + 1) / 2 + r;
+                    X[r] = M::mma(M::join(r <= 2 * m ? mem.Mh[i0 * 64 + lane] : M::none(),
+                                          mem.Mh[i1 * 64 + lane]), yf[m], X[r]);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < KS; ++m) {
+                float y[8];         // the operand's values are dy where X's rows and columns are
+                M::unpack(yf[m], y);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const f4 dq = *reinterpret_cast<const f4 *>(dts + 16 * (2 * m + e) + 4 * g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        IO::store(Ws, (16 * q + 4 * g + i) * LW + 16 * r + l, W[id >> 2][i]);
+                        IO::store(Ud, (16 * (2 * m + e) + 4 * g + i) * LU,
+                                  __builtin_fmaf(dq[i], X[2 * m + e][i], Dh * y[4 * e + i]));
                 }
+            }
+            __builtin_amdgcn_wave_barrier();
+            E *dug = Dp + h * P + p0 + 16 * wv;
+            const int ds = H * P, left = P - p0 - 16 * wv;
+            if constexpr (WIDE) {
+                constexpr int pieces = 16 / V;
+                const Rsrc rd = view(dug, 0x7fffffff);
+                const int c = lane % pieces * V;
+#pragma unroll
+                for (int i = 0; i < Q * pieces / 64; ++i) {
+                    const int t = lane / pieces + i * (64 / pieces);
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        M::template get_perm<u4>(mem.U + t * LU, 16 * wv + c), rd,
+                        t < k.n && c < left ? static_cast<uint32_t>(t * ds + c) * ES : kDrop, 0, 0);
+                }
+            } else {
+                for (int i = lane; i < Q * 16; i += 64) {
+                    const int t = i >> 4, c = i & 15;
+                    if (t < k.n && c < left)
+                        dug[static_cast<int64_t>(t) * ds + c] = mem.U[t * LU + M::pos(16 * wv + c)];
+                }
+            }
+        }
+        __syncthreads();
+        h = hn;
+        p0 = pn;
+    }
+    // ---- W over all heads, rows t by columns s, nothing above the diagonal
+    E *Ws = mem.G;
+    for (int i = tid; i < Q * LW; i += 256) Ws[i] = E(0);
+    put_bc(mem.HC, Cp, a.C_t);
+    __syncthreads();
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        const int r = own_r<TT>(wv, o), q = own_q<TT>(wv, o);
+        if (r < 0) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            IO::store(Ws, (16 * q + 4 * g + i) * LW + M::pos(16 * r + l), W[o][i]);
     }
     __syncthreads();
 #pragma unroll
@@ -724,25 +859,26 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
         if (nt >= NT) break;
 #pragma unroll
         for (int m = 0; m < KS; ++m) {
-            const Frag bf = M::col_perm(Bs + 32 * m * LB + 16 * nt, LB, g, l);
-            const Frag cf = M::col_perm(Cs + 32 * m * LB + 16 * nt, LB, g, l);
+            const Frag bf = M::template col_perm<8>(mem.B + 32 * m * LB + M::pos(16 * nt), LB, g, l);
+            const Frag cf = M::template col_perm<8>(mem.HC + 32 * m * LB + M::pos(16 * nt), LB, g, l);
 #pragma unroll
             for (int q = 0; q < TT; ++q) {
-                dC[q][n] = M::mma(row_nat<IO>(Ws + (16 * q + l) * LW + 32 * m, g), bf, dC[q][n]);
-                dB[q][n] = M::mma(M::col_perm(Ws + 32 * m * LW + 16 * q, LW, g, l), cf, dB[q][n]);
+                dC[q][n] = M::mma(M::row_perm(Ws + (16 * q + l) * LW + 32 * m, g), bf, dC[q][n]);
+                dB[q][n] = M::mma(M::template col_perm<8>(Ws + 32 * m * LW + M::pos(16 * q), LW, g, l), cf,
+                                  dB[q][n]);
             }
         }
         const int col = 16 * nt + l;
-        if (col >= a.N) continue;
+        if (col >= N) continue;
 #pragma unroll
         for (int q = 0; q < TT; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int t = 16 * q + 4 * g + i;
                 if (t >= k.n) continue;
-                const int64_t o = ((k.b * a.L + k.t + t) * a.G + gr) * a.N + col;
+                const int64_t o = ((k.b * a.L + k.t + t) * G + gr) * N + col;
                 if (a.hsplit > 1) {
-                    const int64_t all = a.batch * a.L * a.G * a.N;
+                    const int64_t all = a.batch * a.L * G * N;
                     a.dBp[hs * all + o] = dB[q][n][i];
                     a.dCp[hs * all + o] = dC[q][n][i];
                 } else {
@@ -750,6 +886,95 @@ __global__ __launch_bounds__(256) void heads_chunk_bwd_kernel(HeadsArgs a, int v
                     IO::store(static_cast<E *>(a.dC), o, dC[q][n][i]);
                 }
             }
+    }
+}
+
+// E, and with it ddelta and the chunk's shares of dA, dD and ddelta_bias: a
+// wavefront a head, a lane a token.  E comes without differences of long sums:
+// of the tiles (q, r) of Z those with r < own < q count whole, those of the own
+// row from the token on, those of the own column up to it; only the tile on
+// the diagonal is a difference.
+template <class IO, int Q>
+__global__ __launch_bounds__(256) void heads_grad_kernel(HeadsArgs a, const GradRec<Q> *rec) {
+    using E = typename IO::T;
+    constexpr int TT = Q / 16;
+    const int lane = threadIdx.x & 63, l = lane & 15, own = lane >> 4;
+    const int64_t chunks = a.batch * a.nc, id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (id >= chunks * a.H) return;
+    const int64_t ci = id / a.H, h = id % a.H;
+    const int64_t sph = (a.P + 15) / 16, slices = a.H * sph;
+    const Chunk k = chunk_at(a, ci / a.nc, ci % a.nc);
+    if (k.n <= 0) {
+        if (lane < 3) a.part[(lane * chunks + ci) * a.H + h] = 0.0f;
+        return;
+    }
+    float raw = 0.0f, dt = 0.0f;
+    if (lane < k.n) {
+        raw = IO::load(static_cast<const E *>(a.delta) + k.b * a.dt_b + (k.t + lane) * a.dt_t, h);
+        if (a.bias) raw += a.bias[h];
+        dt = a.softplus ? softplus_exact(raw) : raw;
+    }
+    const double s = lane_prefix(static_cast<double>(dt) * a.A[h] * 1.4426950408889634);
+    const double sQ = lane_value(s, 63);
+    const float dec = exp2_d(sQ);
+    const bool direct = sizeof(E) == 4 || dec < kDirect;
+    const GradRec<Q> &rc = rec[id];
+    float cv = 0.0f, dd = 0.0f, r = 0.0f, p = 0.0f;
+    double rows = 0.0, cols = 0.0, whole = 0.0;
+    if (lane < Q) {
+        const int dg = own * (own + 1) / 2 + own;
+        for (int q = own + 1; q < TT; ++q) {
+            const int at = q * (q + 1) / 2;
+            cv += rc.colv[(at + own) * 16 + l];
+            for (int x = 0; x < own; ++x)
+                for (int i = 0; i < 16; i += 4) {
+                    const f4 w = *reinterpret_cast<const f4 *>(rc.rowz + (at + x) * 16 + i);
+                    whole += (w.x + w.y) + (w.z + w.w);
+                }
+        }
+        cols = static_cast<double>(cv) * dt;
+        for (int x = 0; x < own; ++x) rows += rc.rowz[(own * (own + 1) / 2 + x) * 16 + l];
+        rows += static_cast<double>(rc.rowz[dg * 16 + l]) -
+                static_cast<double>(rc.colv[dg * 16 + l] - rc.diagz[lane]) * dt;
+        cv += rc.colv[dg * 16 + l];
+        dd = rc.diag[lane];
+        const float *rp = a.rp + (ci * slices + h * sph) * Q + lane;
+        for (int64_t i = 0; i < sph; ++i) {
+            r += rp[i * Q];
+            p += rp[chunks * slices * Q + i * Q];
+        }
+        r *= exp2_d(s);
+        p *= exp2_d(sQ - s);
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {      // rows: from the token on; columns: up to it
+        const double x = __shfl_down(rows, o, 16), y = __shfl_up(cols, o, 16);
+        if (l + o < 16) rows += x;
+        if (l >= o) cols += y;
+    }
+    const double before = __shfl_up(cols, 1, 16);
+    const double pd = static_cast<double>(p) * dt;
+    const double rs = lane_prefix(static_cast<double>(r)), ps = lane_prefix(pd);
+    const double X = direct ? static_cast<double>(dec) * ((rc.xdot[0] + rc.xdot[1]) + (rc.xdot[2] + rc.xdot[3]))
+                            : a.through[ci * a.H + h];
+    const double grad = X + (lane_value(rs, 63) - rs + r) + (ps - pd) + whole + rows + (l ? before : 0.0);
+    const float ddt = cv + p + a.A[h] * static_cast<float>(grad);
+    float dr = 0.0f;
+    if (lane < k.n) {
+        dr = a.softplus ? ddt / (1.0f + expf(-raw)) : ddt;
+        IO::store(static_cast<E *>(a.ddelta) + (k.b * a.L + k.t + lane) * a.H, h, dr);
+    }
+    double sA = lane < k.n ? grad * dt : 0.0, sD = lane < k.n ? dd : 0.0f, sb = dr;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        sA += __shfl_xor(sA, o, 64);
+        sD += __shfl_xor(sD, o, 64);
+        sb += __shfl_xor(sb, o, 64);
+    }
+    if (lane == 0) {
+        a.part[ci * a.H + h] = static_cast<float>(sA);
+        a.part[(chunks + ci) * a.H + h] = static_cast<float>(sD);
+        a.part[(2 * chunks + ci) * a.H + h] = static_cast<float>(sb);
     }
 }
 
@@ -784,33 +1009,25 @@ __global__ __launch_bounds__(256) void heads_blocks_kernel(HeadsArgs a) {
 }
 
 // ------------------------------------------------------------------ launch
-template <class IO, int NP, int Q, int PS>
+template <class IO, int NP, int Q, int PS, bool WIDE>
 static hipError_t bwd_go(const HeadsArgs &a, hipStream_t s) {
-    using M = Mat<IO>;
-    using E = typename M::E;
-    constexpr int TT = Q / 16, TRI = TT * (TT + 1) / 2;
-    constexpr int LB = NP + M::kPad, LU = PS + M::kPad;
-    constexpr size_t lds = sizeof(E) * (2 * Q * LB + 2 * Q * LU + 2 * PS * LB + TRI * 256) +
-                           16 * TRI * 64 + 4 * ((4 + TT) * Q + 2 * TRI * 16 + 2 * Q + 4);
+    using E = typename IO::T;
+    constexpr size_t lds = sizeof(ChunkMem<IO, NP, Q, PS>);
     static_assert(lds <= 160 * 1024, "LDS of a compute unit");
-    static_assert(Q * (Q + M::kPad) <= 2 * PS * LB, "W takes the states' place");
+    static_assert(sizeof(GradRec<Q>) <= kGradRec, "workspace of a chunk and head");
     const int64_t hpg = a.H / a.G, sph = (a.P + 15) / 16;
     const int64_t wgs = a.G * ((hpg * sph + 3) / 4), chunks = a.batch * a.nc;
-    const int vecs = (vec_rows<IO>(a.B, a.B_b, a.B_t, a.N) ? 1 : 0) |
-                     (vec_rows<IO>(a.C, a.C_b, a.C_t, a.N) ? 2 : 0) |
-                     (vec_rows<IO>(a.u, a.u_b, a.u_t, a.P) ? 4 : 0) |
-                     (vec_rows<IO>(a.dy, a.dy_b, a.dy_t, a.P) ? 8 : 0) |
-                     (vec_rows<IO>(a.du, 0, a.H * a.P, a.P) ? 16 : 0);
     const unsigned walks = static_cast<unsigned>(2 * wgs * a.J * a.batch);
+    GradRec<Q> *rec = reinterpret_cast<GradRec<Q> *>(a.rec);
     if (a.J > 1) {
-        hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, false>), dim3(walks), dim3(256), 0, s, a, vecs);
+        hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, false, WIDE>), dim3(walks), dim3(256), 0, s, a);
         hipError_t e = launch_heads_join(a, a.hend, a.ldec, 0, s);
         if (e == hipSuccess)
             e = launch_heads_join(a, a.hend + a.batch * a.J * a.H * a.P * a.N,
                                   a.ldec + a.batch * a.J * a.H, 1, s);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, true>), dim3(walks), dim3(256), 0, s, a, vecs);
+    hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, true, WIDE>), dim3(walks), dim3(256), 0, s, a);
     if constexpr (sizeof(E) == 2) {
         hipLaunchKernelGGL(heads_anchor_kernel, dim3(static_cast<unsigned>(a.batch * a.na * a.H)),
                            dim3(64), 0, s, a, NP);
@@ -818,17 +1035,29 @@ static hipError_t bwd_go(const HeadsArgs &a, hipStream_t s) {
                            dim3(static_cast<unsigned>(a.H), static_cast<unsigned>(a.batch)), dim3(64), 0,
                            s, a);
     }
-    hipLaunchKernelGGL((heads_chunk_bwd_kernel<IO, NP, Q, PS>),
-                       dim3(static_cast<unsigned>(chunks * a.G * a.hsplit)), dim3(256), lds, s, a, vecs);
+    hipLaunchKernelGGL((heads_chunk_bwd_kernel<IO, NP, Q, PS, WIDE>),
+                       dim3(static_cast<unsigned>(chunks * a.G * a.hsplit)), dim3(256), lds, s, a, rec);
+    hipLaunchKernelGGL((heads_grad_kernel<IO, Q>), dim3(static_cast<unsigned>((chunks * a.H + 3) / 4)),
+                       dim3(256), 0, s, a, rec);
     return hipGetLastError();
+}
+
+template <class IO, int NP, int Q, int PS>
+static hipError_t bwd_wide(const HeadsArgs &a, hipStream_t s) {
+    const int64_t far = (1LL << 31) / static_cast<int64_t>(sizeof(typename IO::T)) / 64 - 65536;
+    const bool wide = vec_rows<IO>(a.B, a.B_b, a.B_t, a.N) && vec_rows<IO>(a.C, a.C_b, a.C_t, a.N) &&
+                      vec_rows<IO>(a.u, a.u_b, a.u_t, a.P) && vec_rows<IO>(a.dy, a.dy_b, a.dy_t, a.P) &&
+                      vec_rows<IO>(a.du, 0, a.H * a.P, a.P) && a.B_t < far && a.C_t < far &&
+                      a.u_t < far && a.dy_t < far && a.H * a.P < far;
+    return wide ? bwd_go<IO, NP, Q, PS, true>(a, s) : bwd_go<IO, NP, Q, PS, false>(a, s);
 }
 
 template <class IO>
 static hipError_t bwd_io(const HeadsArgs &a, hipStream_t s) {
     constexpr bool f32 = sizeof(typename IO::T) == 4;
     constexpr int Q = f32 ? 32 : 64;
-    hipError_t e = a.N <= 32 ? bwd_go<IO, 32, Q, 64>(a, s) : a.N <= 64 ? bwd_go<IO, 64, Q, 64>(a, s)
-                   : a.N <= 128 ? bwd_go<IO, 128, Q, 64>(a, s) : bwd_go<IO, 256, 32, f32 ? 32 : 64>(a, s);
+    hipError_t e = a.N <= 32 ? bwd_wide<IO, 32, Q, 64>(a, s) : a.N <= 64 ? bwd_wide<IO, 64, Q, 64>(a, s)
+                   : a.N <= 128 ? bwd_wide<IO, 128, Q, 64>(a, s) : bwd_wide<IO, 256, 32, f32 ? 32 : 64>(a, s);
     if (e != hipSuccess) return e;
     if (a.hsplit > 1)
         hipLaunchKernelGGL((heads_blocks_kernel<IO>), dim3(1024, 2), dim3(256), 0, s, a);

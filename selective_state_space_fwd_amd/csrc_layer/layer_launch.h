@@ -63,6 +63,8 @@ hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s);
 
 // Chunks between two float32 copies of the states in the backward.
 constexpr int kAnchor = 2;
+// Bytes that a chunk's products leave for the gradient of its decays.
+constexpr int kGradRec = 1808;
 
 // One chunk of the scan over heads: tokens t .. t + n - 1 of sequence `row`.
 struct HeadsEntry {
@@ -91,7 +93,8 @@ struct HeadsArgs {
     const HeadsEntry *table;    // packed: nc chunks, unused ones with n = 0
     float *hend;                // (2, batch, J, H, P, N) state that enters a range; second: its gradient
     float *ldec;                // (2, batch, J, H) log2 decay of a range, kReset: the range restarts
-    void *hin, *gout;           // (batch nc, H, Pr, Np) io type, P and N padded: states that enter
+    void *hin, *gout;           // (batch nc, H, Pr, Np) io type, P and N padded, in the order of
+                                // the walks' lanes: states that enter
                                 // the chunks, gradients of those that leave them
     float *rp;                  // (2, batch nc, H slices, Q) dot products across chunks, see layer_heads_bwd.hip
     float *rpsum;               // (2, batch nc, H slices) their sums over a chunk's tokens
@@ -101,6 +104,7 @@ struct HeadsArgs {
     float *adot;                // (batch, na, H) their products
     int64_t na;
     float *through;             // (batch nc, H) exp(s_Q) <gout, hin>
+    void *rec;                  // (batch nc, H) sums over the products of a chunk, kGradRec bytes each
     float *part;                // (3, batch nc, H) dA, dD, ddelta_bias of a chunk
     int64_t hsplit, hblk;       // backward: blocks of hblk heads of a group
     float *dBp, *dCp;           // (hsplit, batch, L, G, N) float32 when hsplit > 1

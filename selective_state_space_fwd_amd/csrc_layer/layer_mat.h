@@ -55,6 +55,14 @@ struct Mat<BF16> {
         *reinterpret_cast<uint2 *>(row + pos(c)) = h[0];
         *reinterpret_cast<uint2 *>(row + pos(c + 4)) = h[1];
     }
+    template <class Vec>
+    static __device__ __forceinline__ Vec get_perm(const E *row, int c) {
+        const uint2 h[2] = {*reinterpret_cast<const uint2 *>(row + pos(c)),
+                            *reinterpret_cast<const uint2 *>(row + pos(c + 4))};
+        Vec v;
+        __builtin_memcpy(&v, h, 16);
+        return v;
+    }
     // m: row k = 0 and column 0 of the tile; LDS transposes 4 x 16 values a
     // group.  FOUR: distance of the tile's fours of columns, 8 in rows kept
     // in the permuted order.
@@ -120,7 +128,11 @@ struct Mat<F32> {
     static __device__ __forceinline__ Frag row_perm(const E *p, int g) { return two(p + 4 * g, p + 16 + 4 * g); }
     template <class Vec>
     static __device__ __forceinline__ void put_perm(E *row, int c, const Vec &v) {
-        __builtin_memcpy(__builtin_assume_aligned(row + c, 16), &v, 16);
+        *reinterpret_cast<Vec *>(row + c) = v;
+    }
+    template <class Vec>
+    static __device__ __forceinline__ Vec get_perm(const E *row, int c) {
+        return *reinterpret_cast<const Vec *>(row + c);
     }
     template <int FOUR = 4>
     static __device__ __forceinline__ Frag col_perm(const E *m, int stride, int g, int l) {
