@@ -6,22 +6,33 @@
 
 namespace ssm {
 
-// VW consecutive values of a row as floats: one 16-byte access (8 for VW = 4
-// of 16 bits), or single elements for VW = 1.
+// VW consecutive values of a row as they lie in memory (one access of up to
+// 16 bytes), and as floats.
 template <class IO, int VW>
-__device__ __forceinline__ void load_vec(const typename IO::T *p, float (&o)[VW]) {
-    if constexpr (VW == 1) {
-        o[0] = IO::load(p, 0);
-    } else if constexpr (sizeof(typename IO::T) == 2) {
-        static_assert(VW == 8, "eight 16-bit values");
-        Seg<BF16>::unpack(*reinterpret_cast<const uint4 *>(p), o);
-    } else {
+struct Piece {
+    using T = typename IO::T;
+    static constexpr int kBytes = VW * sizeof(T);
+    uint32_t raw[(kBytes + 3) / 4];
+    __device__ __forceinline__ void load(const T *p) {
+        __builtin_memcpy(raw, __builtin_assume_aligned(p, kBytes < 16 ? kBytes : 16), kBytes);
+    }
+    __device__ __forceinline__ void get(float (&o)[VW]) const {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < VW; i += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + i);
-            o[i] = v.x; o[i + 1] = v.y; o[i + 2] = v.z; o[i + 3] = v.w;
+            for (int i = 0; i < VW; ++i) o[i] = __uint_as_float(raw[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+                o[i] = __uint_as_float(i & 1 ? raw[i / 2] & 0xffff0000u : raw[i / 2] << 16);
         }
     }
+};
+
+template <class IO, int VW>
+__device__ __forceinline__ void load_vec(const typename IO::T *p, float (&o)[VW]) {
+    Piece<IO, VW> v;
+    v.load(p);
+    v.get(o);
 }
 
 template <class IO, int VW>
@@ -29,8 +40,10 @@ __device__ __forceinline__ void store_vec(typename IO::T *p, const float (&o)[VW
     if constexpr (VW == 1) {
         IO::store(p, 0, o[0]);
     } else if constexpr (sizeof(typename IO::T) == 2) {
-        static_assert(VW == 8, "eight 16-bit values");
-        *reinterpret_cast<uint4 *>(p) = Seg<BF16>::pack(o);
+        uint32_t raw[VW / 2];
+#pragma unroll
+        for (int i = 0; i < VW; i += 2) raw[i / 2] = Seg<BF16>::pk(o[i], o[i + 1]);
+        __builtin_memcpy(__builtin_assume_aligned(p, VW * 2), raw, VW * 2);
     } else {
 #pragma unroll
         for (int i = 0; i < VW; i += 4)

@@ -72,23 +72,32 @@ __global__ __launch_bounds__(64) void conv_fwd_kernel(ConvArgs a) {
             float h[W][VW];                     // h[W-1]: the current input
 #pragma unroll
             for (int j = 1; j < W; ++j) input_at<IO, VW, W>(a, q, b, t - W + j, c, h[j]);
-            for (; t < e; ++t) {
+            // the run's tokens all on their way before the first is used
+            const T *x = static_cast<const T *>(a.x) + b * a.x_batch + t * a.x_token + c;
+            Piece<IO, VW> in[kFwdRun];
 #pragma unroll
-                for (int j = 0; j + 1 < W; ++j)
+            for (int n = 0; n < kFwdRun; ++n)
+                if (t + n < e) in[n].load(x + n * a.x_token);
 #pragma unroll
-                    for (int i = 0; i < VW; ++i) h[j][i] = h[j + 1][i];
-                load_vec<IO, VW>(static_cast<const T *>(a.x) + b * a.x_batch + t * a.x_token + c,
-                                 h[W - 1]);
-                float o[VW];
+            for (int n = 0; n < kFwdRun; ++n) {
+                if (t + n < e) {
 #pragma unroll
-                for (int i = 0; i < VW; ++i) {
-                    float v = k.bias[i];
+                    for (int j = 0; j + 1 < W; ++j)
 #pragma unroll
-                    for (int j = 0; j < W; ++j) v = __builtin_fmaf(k.w[j][i], h[j][i], v);
-                    o[i] = a.silu ? silu_f32(v) : v;
+                        for (int i = 0; i < VW; ++i) h[j][i] = h[j + 1][i];
+                    in[n].get(h[W - 1]);
+                    float o[VW];
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) {
+                        float v = k.bias[i];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) v = __builtin_fmaf(k.w[j][i], h[j][i], v);
+                        o[i] = a.silu ? silu_f32(v) : v;
+                    }
+                    store_vec<IO, VW>(static_cast<T *>(a.y) + (b * a.L + t + n) * a.C + c, o);
                 }
-                store_vec<IO, VW>(static_cast<T *>(a.y) + (b * a.L + t) * a.C + c, o);
             }
+            t = e;
             if (a.last && t == q.end) {
 #pragma unroll
                 for (int i = 0; i < VW; ++i)
@@ -118,6 +127,8 @@ __device__ __forceinline__ float act_grad(int silu, float v, float dy) {
     const float s = sigmoid_f32(v);
     return dy * s * __builtin_fmaf(v, 1.0f - s, 1.0f);
 }
+
+constexpr int kBatch = 4;       // tokens that the backward fetches ahead
 
 // Gradients.  With dv = silu'(v) dy: dx_t = sum_k w_k dv_{t+W-1-k},
 // dweight_k = sum_t dv_t x_{t-W+1+k}, dbias = sum_t dv_t.  A run recomputes v
@@ -155,43 +166,62 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
             for (int j = 1; j < W; ++j) input_at<IO, VW, W>(a, q, b, t - W + j, c, h[j]);
             const int64_t from = t;
-            // past e the gradients are zero: the loop runs on to write the last dx
-            for (; t < own + W - 1; ++t) {
-                float dy[VW];
+            const T *x = static_cast<const T *>(a.x) + b * a.x_batch + t * a.x_token + c;
+            const T *y = static_cast<const T *>(a.dy) + b * a.dy_batch + t * a.dy_token + c;
+            // kBatch tokens at a time, the next ones on their way meanwhile
+            Piece<IO, VW> xi[kBatch], yi[kBatch], xn[kBatch], yn[kBatch];
+            auto fetch = [&](int64_t at) {
 #pragma unroll
-                for (int j = 0; j + 1 < W; ++j)
-#pragma unroll
-                    for (int i = 0; i < VW; ++i) { h[j][i] = h[j + 1][i]; g[j][i] = g[j + 1][i]; }
-                if (t < e) {
-                    load_vec<IO, VW>(static_cast<const T *>(a.x) + b * a.x_batch + t * a.x_token +
-                                         c, h[W - 1]);
-                    load_vec<IO, VW>(static_cast<const T *>(a.dy) + b * a.dy_batch +
-                                         t * a.dy_token + c, dy);
-                }
-#pragma unroll
-                for (int i = 0; i < VW; ++i) {
-                    float v = k.bias[i];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) v = __builtin_fmaf(k.w[j][i], h[j][i], v);
-                    g[W - 1][i] = t < e ? act_grad(a.silu, v, dy[i]) : 0.0f;
-                    if (t < own) {
-                        db[i] += g[W - 1][i];
-#pragma unroll
-                        for (int j = 0; j < W; ++j)
-                            dw[j][i] = __builtin_fmaf(g[W - 1][i], h[j][i], dw[j][i]);
+                for (int n = 0; n < kBatch; ++n)
+                    if (from + at + n < e) {
+                        xn[n].load(x + (at + n) * a.x_token);
+                        yn[n].load(y + (at + n) * a.dy_token);
                     }
-                }
-                const int64_t p = t - (W - 1);  // the token whose last dv this was
-                if (p >= from) {
-                    float o[VW];
+            };
+            fetch(0);
+            // past e the gradients are zero: the loop runs on to write the last dx
+            while (t < own + W - 1) {
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) { xi[n] = xn[n]; yi[n] = yn[n]; }
+                fetch(t - from + kBatch);
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) {
+                    if (t >= own + W - 1) break;
+                    float dy[VW];
+#pragma unroll
+                    for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+                        for (int i = 0; i < VW; ++i) { h[j][i] = h[j + 1][i]; g[j][i] = g[j + 1][i]; }
+                    if (t < e) {
+                        xi[n].get(h[W - 1]);
+                        yi[n].get(dy);
+                    }
 #pragma unroll
                     for (int i = 0; i < VW; ++i) {
-                        float v = 0.0f;
+                        float v = k.bias[i];
 #pragma unroll
-                        for (int j = 0; j < W; ++j) v = __builtin_fmaf(k.w[W - 1 - j][i], g[j][i], v);
-                        o[i] = v;
+                        for (int j = 0; j < W; ++j) v = __builtin_fmaf(k.w[j][i], h[j][i], v);
+                        g[W - 1][i] = t < e ? act_grad(a.silu, v, dy[i]) : 0.0f;
+                        if (t < own) {
+                            db[i] += g[W - 1][i];
+#pragma unroll
+                            for (int j = 0; j < W; ++j)
+                                dw[j][i] = __builtin_fmaf(g[W - 1][i], h[j][i], dw[j][i]);
+                        }
                     }
-                    store_vec<IO, VW>(static_cast<T *>(a.dx) + (b * a.L + p) * a.C + c, o);
+                    const int64_t p = t - (W - 1);  // the token whose last dv this was
+                    if (p >= from) {
+                        float o[VW];
+#pragma unroll
+                        for (int i = 0; i < VW; ++i) {
+                            float v = 0.0f;
+#pragma unroll
+                            for (int j = 0; j < W; ++j) v = __builtin_fmaf(k.w[W - 1 - j][i], g[j][i], v);
+                            o[i] = v;
+                        }
+                        store_vec<IO, VW>(static_cast<T *>(a.dx) + (b * a.L + p) * a.C + c, o);
+                    }
+                    ++t;
                 }
             }
             t = own;
@@ -243,24 +273,24 @@ __global__ __launch_bounds__(256) void conv_dstate_kernel(ConvArgs a) {
     }
 }
 
-// dweight and dbias: the runs' partial rows, added in order.  64 columns by
-// 4 wavefronts, each a quarter of the runs.
+// dweight and dbias: the runs' partial rows, added in a fixed order: 32 columns
+// by 16 lanes, each every 16th run, then the 16 in a tree.
 template <int W>
-__global__ __launch_bounds__(256) void conv_reduce_kernel(ConvArgs a) {
-    __shared__ float sum[4][64];
+__global__ __launch_bounds__(512) void conv_reduce_kernel(ConvArgs a) {
+    __shared__ float sum[16][33];
     const int64_t cols = (W + 1) * a.C;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
-    const int w = threadIdx.x >> 6;
-    const int64_t per = (a.runs + 3) / 4;
-    const int64_t r1 = (w + 1) * per < a.runs ? (w + 1) * per : a.runs;
+    const int x = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + x;
     float v = 0.0f;
     if (col < cols)
-        for (int64_t r = w * per; r < r1; ++r) v += a.part[r * cols + col];
-    sum[w][threadIdx.x & 63] = v;
-    __syncthreads();
+        for (int64_t r = w; r < a.runs; r += 16) v += a.part[r * cols + col];
+    sum[w][x] = v;
+    for (int n = 8; n > 0; n >>= 1) {
+        __syncthreads();
+        if (w < n) sum[w][x] += sum[w + n][x];
+    }
     if (w || col >= cols) return;
-    const int l = threadIdx.x;
-    v = (sum[0][l] + sum[1][l]) + (sum[2][l] + sum[3][l]);
+    v = sum[0][x];
     const int64_t k = col / a.C, c = col % a.C;
     if (k < W) a.dweight[c * W + k] = v;
     else if (a.dbias) a.dbias[c] = v;
@@ -346,7 +376,7 @@ static hipError_t conv_bwd_w(const ConvArgs &a, hipStream_t s) {
     if (a.runs > 0)
         hipLaunchKernelGGL((conv_bwd_kernel<IO, VW, W>), dim3(gx, grid_y(a.runs)), dim3(64), 0, s, a);
     hipLaunchKernelGGL((conv_reduce_kernel<W>),
-                       dim3(static_cast<unsigned>(((W + 1) * a.C + 63) / 64)), dim3(256), 0, s, a);
+                       dim3(static_cast<unsigned>(((W + 1) * a.C + 31) / 32)), dim3(512), 0, s, a);
     if (W > 1 && a.dstate && a.rows > 0)
         hipLaunchKernelGGL((conv_dstate_kernel<IO, W>),
                            dim3(static_cast<unsigned>((a.C + 255) / 256), grid_y(a.rows)),
@@ -362,6 +392,8 @@ static hipError_t conv_update_w(const ConvArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// In bfloat16 the backward takes 8 bytes a lane: 16 would need twice the
+// registers for its taps and sums and give half the wavefronts.
 #define CONV_BY_WIDTH(NAME, BWD)                                                     \
     template <class IO, int VW>                                                      \
     static hipError_t NAME##_io(const ConvArgs &a, hipStream_t s) {                  \
@@ -370,7 +402,7 @@ static hipError_t conv_update_w(const ConvArgs &a, hipStream_t s) {
     }                                                                                \
     hipError_t launch_##NAME(const ConvArgs &a, hipStream_t s) {                     \
         if (a.bf16)                                                                  \
-            return conv_vec<BF16>(a, BWD) ? NAME##_io<BF16, 8>(a, s) : NAME##_io<BF16, 1>(a, s); \
+            return conv_vec<BF16>(a, BWD) ? NAME##_io<BF16, BWD ? 4 : 8>(a, s) : NAME##_io<BF16, 1>(a, s); \
         return conv_vec<F32>(a, BWD) ? NAME##_io<F32, 4>(a, s) : NAME##_io<F32, 1>(a, s); \
     }
 CONV_BY_WIDTH(conv_fwd, false)

@@ -13,13 +13,24 @@ __global__ __launch_bounds__(256) void heads_join_kernel(HeadsArgs a, float *hen
     const int64_t per = a.P * a.N, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t h = blockIdx.y % a.H, b = blockIdx.y / a.H;
     if (i >= per) return;
+    // eight ranges on their way at a time
     float v = 0.0f;
-    for (int64_t x = 0; x < a.J; ++x) {
-        const int64_t j = b * a.J + (reverse ? a.J - 1 - x : x);
-        float *p = hend + (j * a.H + h) * per + i;
-        const float d = ldec[j * a.H + h];
-        v = d == -INFINITY ? *p : __builtin_fmaf(exp2_hw(d), v, *p);
-        *p = v;
+    for (int64_t x0 = 0; x0 < a.J; x0 += 8) {
+        float in[8], d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t x = x0 + e < a.J ? x0 + e : a.J - 1;
+            const int64_t j = b * a.J + (reverse ? a.J - 1 - x : x);
+            in[e] = hend[(j * a.H + h) * per + i];
+            d[e] = ldec[j * a.H + h];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (x0 + e < a.J) {
+                const int64_t j = b * a.J + (reverse ? a.J - 1 - x0 - e : x0 + e);
+                v = d[e] == -INFINITY ? in[e] : __builtin_fmaf(exp2_hw(d[e]), v, in[e]);
+                hend[(j * a.H + h) * per + i] = v;
+            }
     }
 }
 

@@ -51,11 +51,11 @@ struct WalkMem {
     __attribute__((aligned(16))) float tok[4][Q];
 };
 
+// Wavefronts a SIMD to hold the registers to, as in the forward walk (128
+// states in bfloat16: 167 registers, three workgroups a compute unit).
 template <class IO, int NP, int Q, bool FULL>
 constexpr int walk_waves() {
-    constexpr int n = static_cast<int>(160 * 1024 / sizeof(WalkMem<IO, NP, Q, FULL>));
-    constexpr int r = NP > 128 ? 1 : sizeof(typename IO::T) == 4 && FULL ? 2 : 3;
-    return n < 1 ? 1 : n > r ? r : n;
+    return NP > 128 || 2 * sizeof(WalkMem<IO, NP, Q, FULL>) > 160 * 1024 ? 1 : 2;
 }
 
 // DIR 0: state from u and B, dotted with C and dy.  DIR 1 (against time): gh
@@ -75,8 +75,9 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
     static_assert(Q * PB % 256 == 0 && Q * PU % 256 == 0, "whole rounds of the workgroup");
     __shared__ Mem mem;
 
-    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lane = tid & 63, g = lane >> 4, l = lane & 15;
+    int tid = threadIdx.x;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, g = lane >> 4, l = lane & 15;
     const int N = static_cast<int>(a.N), P = static_cast<int>(a.P), H = static_cast<int>(a.H);
     const int hpg = static_cast<int>(a.H / a.G), sph = (P + 15) / 16, per = (hpg * sph + 3) / 4;
     const int wgs = static_cast<int>(a.G) * per, J = static_cast<int>(a.J);
@@ -227,6 +228,8 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
         put_ry();
     }
     for (int x = c0; x < c1; ++x) {
+        // addresses are made here, not kept (and spilled) over the walk
+        asm volatile("" : "+v"(l), "+v"(g), "+v"(lane), "+v"(tid));
         const Chunk k = next;
         const int64_t c = row0 + (dir ? c0 + c1 - 1 - x : x);
         if (x + 1 < c1) next = chunk(x + 1); else next.n = 0;
@@ -269,11 +272,11 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
         __syncthreads();
         if (FULL && k.n > 0) {
             // ---- leave the state: a lane's values side by side
-            E *to = static_cast<E *>(dir ? a.gout : a.hin) + ((c * slices + slice) * NT * 64 + lane) * 4;
             if (!idle) {
+                const Rsrc to = view(static_cast<E *>(dir ? a.gout : a.hin) + (c * slices + slice) * NT * 256,
+                                     NT * 256 * ES);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    *reinterpret_cast<typename M::Half *>(to + nt * 256) = M::half(S[nt]);
+                for (int nt = 0; nt < NT; ++nt) M::store(M::half(S[nt]), to, lane * 4 * ES, nt * 256 * ES);
                 if (sizeof(E) == 2 && k.first) {
                     // X of a first chunk needs the product with the start state
                     if (dir == 1 && a.h0) {
@@ -290,10 +293,11 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
                         if (lane == 0) a.hdot[k.row * slices + slice] = v;
                     }
                 } else if (sizeof(E) == 2 && (c - row0) % kAnchor == 0 && dec >= kDirect) {
-                    f4 *an = reinterpret_cast<f4 *>(a.anchor) +
-                             (((dir * a.batch + b) * a.na + (c - row0) / kAnchor) * slices + slice) * NT * 64 + lane;
+                    const Rsrc an = view(
+                        a.anchor + (((dir * a.batch + b) * a.na + (c - row0) / kAnchor) * slices + slice) * NT * 256,
+                        NT * 256 * 4);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) an[nt * 64] = S[nt];
+                    for (int nt = 0; nt < NT; ++nt) store16(S[nt], an, lane * 16, nt * 1024);
                 }
                 if (sizeof(E) == 2 && dir == 0 && p0 == 0 && lane == 0) a.through[c * H + h] = dec;
             }
@@ -316,7 +320,8 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
                     for (int q = 0; q < TT; ++q) Y[q] = M::mma(rf[q], hf[z], Y[q]);
             }
             float total = 0.0f;
-            float *rp = a.rp + ((dir * chunks + c) * slices + slice) * Q;
+            const Rsrc rp = view(a.rp + ((dir * chunks + c) * slices + slice) * Q, idle ? 0 : Q * 4);
+            const uint32_t ro_ = l == 0 ? g * 16 : kDrop;
 #pragma unroll
             for (int m = 0; m < KS; ++m) {
                 float y[8];     // the operand's values are where the result's are
@@ -328,7 +333,7 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
 #pragma unroll
                     for (int i = 0; i < 4; ++i) d[i] = row_sum(Y[q][i] * y[4 * e + i]);
                     // kept without the decay (and dt) to the chunk's end
-                    if (l == 0 && !idle) *reinterpret_cast<f4 *>(rp + 16 * q + 4 * g) = d;
+                    store16(d, rp, ro_, 64 * q);
                     if (sizeof(E) == 4) continue;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) d[i] *= __shfl(ts, 16 * q + 4 * g + i, 64);
@@ -384,22 +389,26 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
     }
 }
 
-// <gh, h_in> of every kAnchor-th chunk that keeps kDirect, a wavefront a head;
+// <gh, h_in> of every kAnchor-th chunk that keeps kDirect, a workgroup a head;
 // of no meaning, and not used, where a sequence begins.
-__global__ __launch_bounds__(64) void heads_anchor_kernel(HeadsArgs a, int np) {
+__global__ __launch_bounds__(256) void heads_anchor_kernel(HeadsArgs a, int np) {
     const int64_t h = blockIdx.x % a.H, x = blockIdx.x / a.H;      // x: batch row and anchor
     const int64_t sph = (a.P + 15) / 16, per = sph * 4 * np;       // f4s of one head
     const int64_t all = a.batch * a.na * a.H * per;
     const int64_t c = x / a.na * a.nc + x % a.na * kAnchor;
     if (a.through[c * a.H + h] < kDirect) return;
     const f4 *p = reinterpret_cast<const f4 *>(a.anchor) + (x * a.H + h) * per;
+    __shared__ double sum[4];
     double v = 0.0;
-    for (int64_t i = threadIdx.x; i < per; i += 64) {
+    for (int64_t i = threadIdx.x; i < per; i += 256) {
         const f4 q = p[i] * p[all + i];
         v += static_cast<double>((q.x + q.y) + (q.z + q.w));
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     if (threadIdx.x == 0) a.adot[x * a.H + h] = static_cast<float>(v);
 }
 
@@ -516,8 +525,9 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     extern __shared__ __attribute__((aligned(16))) unsigned char raw[];
     Mem &mem = *reinterpret_cast<Mem *>(raw);
 
-    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lane = tid & 63, g = lane >> 4, l = lane & 15;
+    int tid = threadIdx.x;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, g = lane >> 4, l = lane & 15;
     const int N = static_cast<int>(a.N), P = static_cast<int>(a.P), H = static_cast<int>(a.H);
     const int G = static_cast<int>(a.G), hpg = H / G, sph = (P + 15) / 16;
     const int id = static_cast<int>(by_xcd(blockIdx.x, gridDim.x));
@@ -552,7 +562,7 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         }
     };
 
-    // ---- the next head's tokens and states on their way in registers
+    // ---- a head's tokens and states on their way in registers
     u4 Ur[NU], Yr[NU], Hr[NS], Gr[NS];
     uint32_t uo = 0, yo = 0;
     float dtr = 0.0f;
@@ -605,21 +615,30 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
 
     put_bc(mem.B, Bp, a.B_t);
     put_bc(mem.HC, Cp, a.C_t);
-    fetch(h0, 0);
-    fetch_states(h0, 0);
     __syncthreads();
     f4 CB[OWN], W[OWN], DX[OWN], dB[TT][NW], dC[TT][NW];
     const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int o = 0; o < OWN; ++o) {             // C_t . B_s: rows t, columns s
-        W[o] = CB[o] = DX[o] = zero;
-        const int r = own_r<TT>(wv, o), q = own_q<TT>(wv, o);
-        if (r >= 0)
+    for (int o = 0; o < OWN; ++o) W[o] = CB[o] = DX[o] = zero;
+    // one version of the tiles' work a wavefront, its tiles known
+    auto by_wave = [&](auto f) {
+        if (wv == 0) f(Int<0>());
+        else if (wv == 1) f(Int<1>());
+        else if (wv == 2) f(Int<2>());
+        else f(Int<3>());
+    };
+    by_wave([&](auto w) {                       // C_t . B_s: rows t, columns s
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            constexpr int WV = decltype(w)::value;
+            const int r = own_r<TT>(WV, o), q = own_q<TT>(WV, o);
+            if (r < 0) continue;
 #pragma unroll
             for (int m = 0; m < KN; ++m)
                 CB[o] = M::mma(M::row_perm(mem.HC + (16 * q + l) * LB + 32 * m, g),
                                M::row_perm(mem.B + (16 * r + l) * LB + 32 * m, g), CB[o]);
-    }
+        }
+    });
 #pragma unroll
     for (int q = 0; q < TT; ++q)
 #pragma unroll
@@ -630,9 +649,14 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     float xdot = 0.0f;
     int h = h0, p0 = 0;
     while (h < h1) {
+        // addresses are made here, not kept (and spilled) over the loop
+        asm volatile("" : "+v"(l), "+v"(g), "+v"(lane), "+v"(tid));
         const double A2 = static_cast<double>(a.A[h]) * 1.4426950408889634;
         const float Dh = a.D ? a.D[h] : 0.0f;
-        // ---- stage
+        // ---- stage.  Not fetched ahead: two workgroups share the compute unit,
+        // and with the sums of dB and dC there are no registers to wait in
+        fetch(h, p0);
+        fetch_states(h, p0);
         if constexpr (WIDE) {
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
@@ -670,7 +694,6 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         }
         const int hn = p0 + PS < P ? h : h + 1, pn = p0 + PS < P ? p0 + PS : 0;
         const bool last = hn != h;
-        if (hn < h1) fetch(hn, pn);
         if (p0 == 0 && lane < Q) {
             double ref[TT];
             ref[0] = 0.0;
@@ -698,9 +721,11 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
 #pragma unroll
             for (int o = 0; o < OWN; ++o) DX[o] = zero;
         }
+        by_wave([&](auto w) {
+        constexpr int WV = decltype(w)::value;
 #pragma unroll
         for (int o = 0; o < OWN; ++o) {
-            const int r = own_r<TT>(wv, o), q = own_q<TT>(wv, o), idx = q * (q + 1) / 2 + r;
+            const int r = own_r<TT>(WV, o), q = own_q<TT>(WV, o), idx = q * (q + 1) / 2 + r;
             if (r < 0) continue;
 #pragma unroll
             for (int m = 0; m < KP; ++m)
@@ -739,6 +764,7 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
                 if (l == 0) *reinterpret_cast<f4 *>(rc->rowz + idx * 16 + 4 * g) = row;
             }
         }
+        });
         if (last && direct) {
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) xdot += __shfl_xor(xdot, o, 64);
@@ -746,31 +772,41 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         }
         if (last) xdot = 0.0f;
         // ---- what the states give dC and dB: a quarter of the columns n a wavefront
+        if (NT >= 4 || wv < NT) {
+            Frag hf[NW][KP], gf[NW][KP];
 #pragma unroll
-        for (int n = 0; n < NW; ++n) {
-            const int nt = wv * NW + n;
-            if (nt >= NT) break;
-            Frag hf[KP], gf[KP];
-#pragma unroll
-            for (int m = 0; m < KP; ++m) {
-                hf[m] = M::template col_perm<8>(mem.HC + 32 * m * LB + M::pos(16 * nt), LB, g, l);
-                gf[m] = M::template col_perm<8>(mem.G + 32 * m * LB + M::pos(16 * nt), LB, g, l);
-            }
-#pragma unroll
-            for (int q = 0; q < TT; ++q) {
-                f4 x = zero, y = zero;
+            for (int n = 0; n < NW; ++n)
 #pragma unroll
                 for (int m = 0; m < KP; ++m) {
-                    x = M::mma(M::row_perm(mem.Y + (16 * q + l) * LU + 32 * m, g), hf[m], x);
-                    y = M::mma(M::row_perm(mem.U + (16 * q + l) * LU + 32 * m, g), gf[m], y);
+                    const int at = 32 * m * LB + M::pos(16 * n) + (NW == 1 ? M::pos(16 * wv) : 16 * NW * wv);
+                    hf[n][m] = M::template col_perm<FOUR>(mem.HC + at, LB, g, l);
+                    gf[n][m] = M::template col_perm<FOUR>(mem.G + at, LB, g, l);
                 }
-                dC[q][n] += *reinterpret_cast<const f4 *>(es + 16 * q + 4 * g) * x;
-                dB[q][n] += *reinterpret_cast<const f4 *>(we + 16 * q + 4 * g) *
-                            *reinterpret_cast<const f4 *>(dts + 16 * q + 4 * g) * y;
+#pragma unroll
+            for (int q = 0; q < TT; ++q) {
+                f4 x[NW], y[NW];
+#pragma unroll
+                for (int n = 0; n < NW; ++n) x[n] = y[n] = zero;
+#pragma unroll
+                for (int m = 0; m < KP; ++m) {
+                    const Frag yr = M::row_perm(mem.Y + (16 * q + l) * LU + 32 * m, g);
+                    const Frag ur = M::row_perm(mem.U + (16 * q + l) * LU + 32 * m, g);
+#pragma unroll
+                    for (int n = 0; n < NW; ++n) {
+                        x[n] = M::mma(yr, hf[n][m], x[n]);
+                        y[n] = M::mma(ur, gf[n][m], y[n]);
+                    }
+                }
+                const f4 e = *reinterpret_cast<const f4 *>(es + 16 * q + 4 * g);
+                const f4 w = *reinterpret_cast<const f4 *>(we + 16 * q + 4 * g) *
+                             *reinterpret_cast<const f4 *>(dts + 16 * q + 4 * g);
+#pragma unroll
+                for (int n = 0; n < NW; ++n) {
+                    dC[q][n] += e * x[n];
+                    dB[q][n] += w * y[n];
+                }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        if (hn < h1) fetch_states(hn, pn);
         // ---- du of 16 channels a wavefront: first what gh gives
         f4 X[TT];
         if (16 * wv < PS) {
@@ -792,7 +828,7 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
             Frag yf[KS];
 #pragma unroll
             for (int m = 0; m < KS; ++m) {
-                yf[m] = M::template col_perm<8>(mem.Y + 32 * m * LU + M::pos(16 * wv), LU, g, l);
+                yf[m] = M::template col_perm<FOUR>(mem.Y + 32 * m * LU + M::pos(16 * wv), LU, g, l);
 #pragma unroll
                 for (int r = 0; r < 2 * m + 2; ++r) {
                     const int i1 = (2 * m + 1) * (2 * m + 2) / 2 + r, i0 = 2 * m * (2 * m + 1) / 2 + r;
@@ -859,12 +895,12 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         if (nt >= NT) break;
 #pragma unroll
         for (int m = 0; m < KS; ++m) {
-            const Frag bf = M::template col_perm<8>(mem.B + 32 * m * LB + M::pos(16 * nt), LB, g, l);
-            const Frag cf = M::template col_perm<8>(mem.HC + 32 * m * LB + M::pos(16 * nt), LB, g, l);
+            const Frag bf = M::template col_perm<FOUR>(mem.B + 32 * m * LB + M::pos(16 * nt), LB, g, l);
+            const Frag cf = M::template col_perm<FOUR>(mem.HC + 32 * m * LB + M::pos(16 * nt), LB, g, l);
 #pragma unroll
             for (int q = 0; q < TT; ++q) {
                 dC[q][n] = M::mma(M::row_perm(Ws + (16 * q + l) * LW + 32 * m, g), bf, dC[q][n]);
-                dB[q][n] = M::mma(M::template col_perm<8>(Ws + 32 * m * LW + M::pos(16 * q), LW, g, l), cf,
+                dB[q][n] = M::mma(M::template col_perm<FOUR>(Ws + 32 * m * LW + M::pos(16 * q), LW, g, l), cf,
                                   dB[q][n]);
             }
         }
@@ -1000,8 +1036,23 @@ __global__ __launch_bounds__(256) void heads_blocks_kernel(HeadsArgs a) {
     E *out = static_cast<E *>(blockIdx.y ? a.dC : a.dB);
     int64_t end = n;
     if (a.cu) end = seq_at(a.cu, a.rows, a.L) * a.G * a.N;      // tokens behind the last sequence
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < end;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
+    // four at a time (whole: n and end are multiples of N) where N allows it
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+    if (a.N % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0) {
+        for (int64_t i = first * 4; i < end; i += step * 4) {
+            f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int64_t x = 0; x < a.hsplit; ++x) v += *reinterpret_cast<const f4 *>(p + x * n + i);
+            if constexpr (sizeof(E) == 2)
+                *reinterpret_cast<uint2 *>(out + i) =
+                    make_uint2(Seg<BF16>::pk(v.x, v.y), Seg<BF16>::pk(v.z, v.w));
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[i + e] = v[e];
+        }
+        return;
+    }
+    for (int64_t i = first; i < end; i += step) {
         float v = 0.0f;
         for (int64_t x = 0; x < a.hsplit; ++x) v += p[x * n + i];
         IO::store(out, i, v);
@@ -1030,7 +1081,7 @@ static hipError_t bwd_go(const HeadsArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, true, WIDE>), dim3(walks), dim3(256), 0, s, a);
     if constexpr (sizeof(E) == 2) {
         hipLaunchKernelGGL(heads_anchor_kernel, dim3(static_cast<unsigned>(a.batch * a.na * a.H)),
-                           dim3(64), 0, s, a, NP);
+                           dim3(256), 0, s, a, NP);
         hipLaunchKernelGGL(heads_through_kernel,
                            dim3(static_cast<unsigned>(a.H), static_cast<unsigned>(a.batch)), dim3(64), 0,
                            s, a);

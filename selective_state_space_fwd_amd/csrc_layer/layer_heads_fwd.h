@@ -62,8 +62,6 @@ struct FwdMem {
 // Which tiles (q, r) of C_t . B_s wavefront w computes, o = 0, 1, ...; r < 0:
 // none.  Four rows of tiles: the last row's first three, the third row, the
 // second row, the first and the last.  Two rows: one each.
-template <int I>
-struct Int { static constexpr int value = I; };
 template <int TT>
 __device__ __forceinline__ constexpr int deal_q(int w, int o) {
     if constexpr (TT == 2) return w == 0 ? 0 : 1;
@@ -75,12 +73,13 @@ __device__ __forceinline__ constexpr int deal_r(int w, int o) {
     return w == 3 ? (o == 0 ? 0 : o == 1 ? 3 : -1) : o <= (w == 2 ? 1 : 2) ? o : -1;
 }
 
-// Wavefronts a SIMD that the LDS leaves room for, where the registers reach.
+// Wavefronts a SIMD to hold the registers to: two (one where the LDS has no
+// room for more, or above 128 states).  At 128 states in bfloat16 the kernel
+// then takes 165 registers, and three workgroups fit; held to three it takes
+// 135 and is slower (8 x 2048 x 80 heads: 234 against 243 us).
 template <class IO, int NP, int HW, int Q, bool FULL>
 constexpr int fwd_waves() {
-    constexpr int n = static_cast<int>(160 * 1024 / sizeof(FwdMem<IO, NP, HW, Q, FULL>));
-    constexpr int r = NP > 128 ? 1 : sizeof(typename IO::T) == 4 && FULL ? 2 : 3;
-    return n < 1 ? 1 : n > r ? r : n;
+    return NP > 128 || 2 * sizeof(FwdMem<IO, NP, HW, Q, FULL>) > 160 * 1024 ? 1 : 2;
 }
 
 // WIDE: rows of B, C, u and y in 16-byte pieces, a chunk's within 2^31 bytes,
@@ -99,8 +98,9 @@ __global__ __launch_bounds__(256, (fwd_waves<IO, NP, HW, Q, FULL>())) void heads
     static_assert(Q * PB % 256 == 0 && Q * PU % 256 == 0, "whole rounds of the workgroup");
     __shared__ Mem mem;
 
-    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lane = tid & 63, g = lane >> 4, l = lane & 15;
+    int tid = threadIdx.x;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, g = lane >> 4, l = lane & 15;
     const int id = static_cast<int>(by_xcd(blockIdx.x, gridDim.x));
     const int wg = id % a.wgs, j = id / a.wgs % a.J, b = id / (a.wgs * a.J);
     const int gr = wg / a.per, in = wg % a.per;
@@ -242,6 +242,8 @@ __global__ __launch_bounds__(256, (fwd_waves<IO, NP, HW, Q, FULL>())) void heads
         put_c();
     }
     for (int c = c0; c < c1; ++c) {
+        // addresses are made here, not kept (and spilled) over the walk
+        asm volatile("" : "+v"(l), "+v"(g), "+v"(lane), "+v"(tid));
         const Chunk k = next;
         if (k.n <= 0) break;                    // unused chunks lie behind the used ones
         if (k.first) {

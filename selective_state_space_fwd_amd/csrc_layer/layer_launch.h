@@ -34,7 +34,7 @@ struct ConvArgs {
     const int32_t *slots;       // (batch) or null: row i is slot i
     int64_t n_slots;
 };
-constexpr int kConvBwdRun = 64;  // tokens of one backward run (one partial sum of dweight)
+constexpr int kConvBwdRun = 32;  // tokens of one backward run (one partial sum of dweight)
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_update(const ConvArgs &a, hipStream_t s);

@@ -23,6 +23,15 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
+__device__ __forceinline__ void store16(f4 v, Rsrc to, uint32_t off, int more) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), to, off, more, 0);
+}
+
+// A number known while compiling, for lambdas.
+template <int I>
+struct Int { static constexpr int value = I; };
+
 template <class IO>
 struct Mat;
 
@@ -90,6 +99,10 @@ struct Mat<BF16> {
     static __device__ __forceinline__ Half half(f4 v) {
         return make_uint2(Seg<BF16>::pk(v.x, v.y), Seg<BF16>::pk(v.z, v.w));
     }
+    static __device__ __forceinline__ void store(Half h, Rsrc to, uint32_t off, int more) {
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b64(u2{h.x, h.y}, to, off, more, 0);
+    }
     static __device__ __forceinline__ Half none() { return make_uint2(0, 0); }
     static __device__ __forceinline__ Frag join(Half a, Half b) {
         Bits x;
@@ -150,6 +163,9 @@ struct Mat<F32> {
     }
     using Half = f4;
     static __device__ __forceinline__ Half half(f4 v) { return v; }
+    static __device__ __forceinline__ void store(Half h, Rsrc to, uint32_t off, int more) {
+        store16(h, to, off, more);
+    }
     static __device__ __forceinline__ Half none() { return f4{0.0f, 0.0f, 0.0f, 0.0f}; }
     static __device__ __forceinline__ Frag join(Half a, Half b) {
         return Frag{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};

@@ -222,23 +222,21 @@ __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
     }
 }
 
-// dweight: the workgroups' partial rows, added in order: 64 columns by 4
-// wavefronts, each a quarter of the rows.
-__global__ __launch_bounds__(256) void norm_reduce_kernel(NormArgs a) {
-    __shared__ float sum[4][64];
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
-    const int w = threadIdx.x >> 6;
-    const int64_t per = (a.nblk + 3) / 4;
-    const int64_t r1 = (w + 1) * per < a.nblk ? (w + 1) * per : a.nblk;
+// dweight: the workgroups' partial rows, added in a fixed order: 32 columns by
+// 16 lanes, each every 16th row, then the 16 in a tree.
+__global__ __launch_bounds__(512) void norm_reduce_kernel(NormArgs a) {
+    __shared__ float sum[16][33];
+    const int x = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
     float v = 0.0f;
     if (c < a.d)
-        for (int64_t r = w * per; r < r1; ++r) v += a.part[r * a.d + c];
-    sum[w][threadIdx.x & 63] = v;
-    __syncthreads();
-    if (w == 0 && c < a.d) {
-        const int l = threadIdx.x;
-        a.dweight[c] = (sum[0][l] + sum[1][l]) + (sum[2][l] + sum[3][l]);
+        for (int64_t r = w; r < a.nblk; r += 16) v += a.part[r * a.d + c];
+    sum[w][x] = v;
+    for (int n = 8; n > 0; n >>= 1) {
+        __syncthreads();
+        if (w < n) sum[w][x] += sum[w + n][x];
     }
+    if (w == 0 && c < a.d) a.dweight[c] = sum[0][x];
 }
 
 // ------------------------------------------------------------------ launch
@@ -273,7 +271,7 @@ static hipError_t norm_go(const NormArgs &a, bool bwd, int threads, hipStream_t 
         hipLaunchKernelGGL((norm_bwd_kernel<IO, RT, VW, NV>),
                            dim3(static_cast<unsigned>(a.nblk), static_cast<unsigned>(ng)),
                            dim3(threads), 0, s, a);
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((a.d + 63) / 64)), dim3(256),
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), dim3(512),
                        0, s, a);
     return hipGetLastError();
 }
