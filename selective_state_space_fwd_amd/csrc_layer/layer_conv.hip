@@ -3,7 +3,7 @@
 //
 // Forward, gradients and the single-token step are streams: each input is
 // read and each output written once, and a few multiplications per value lie
-// far below the vector rate, so HBM bounds them.  A lane owns 16 bytes of
+// far below the vector rate, so HBM bounds them.  A lane owns four
 // neighbouring channels and walks a run of tokens with the last W - 1 inputs
 // in registers; the runs' W - 1 overlapping tokens come from the caches.
 #include "layer_common.h"
@@ -345,16 +345,18 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvArgs a) {
 
 // ------------------------------------------------------------------ launch
 static bool al16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+template <class IO>
+static bool al4(const void *p) { return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(typename IO::T)) == 0; }
 static unsigned grid_y(int64_t n) { return static_cast<unsigned>(n < 65535 ? n : 65535); }
 
-// 16-byte accesses need whole vectors of channels and aligned rows.
+// Four channels at a time need whole fours and aligned rows.
 template <class IO>
 static bool conv_vec(const ConvArgs &a, bool bwd) {
-    constexpr int V = Seg<IO>::VW;
-    bool ok = a.C % V == 0 && al16(a.x) && a.x_token % V == 0 && a.x_batch % V == 0;
-    if (bwd) ok = ok && al16(a.dy) && a.dy_token % V == 0 && a.dy_batch % V == 0 && al16(a.dx) &&
+    constexpr int V = 4;
+    bool ok = a.C % V == 0 && al4<IO>(a.x) && a.x_token % V == 0 && a.x_batch % V == 0;
+    if (bwd) ok = ok && al4<IO>(a.dy) && a.dy_token % V == 0 && a.dy_batch % V == 0 && al4<IO>(a.dx) &&
                   al16(a.part);
-    else ok = ok && al16(a.y);
+    else ok = ok && al4<IO>(a.y);
     return ok && (!a.slot_state || al16(a.slot_state));
 }
 
@@ -392,8 +394,9 @@ static hipError_t conv_update_w(const ConvArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// In bfloat16 the backward takes 8 bytes a lane: 16 would need twice the
-// registers for its taps and sums and give half the wavefronts.
+// Bfloat16 goes by 8 bytes a lane: 16 would need twice the registers for taps,
+// tokens on their way and sums, and give half the wavefronts (forward, 8 x
+// 2048 x 5376: 80 against 90 us).
 #define CONV_BY_WIDTH(NAME, BWD)                                                     \
     template <class IO, int VW>                                                      \
     static hipError_t NAME##_io(const ConvArgs &a, hipStream_t s) {                  \
@@ -402,7 +405,7 @@ static hipError_t conv_update_w(const ConvArgs &a, hipStream_t s) {
     }                                                                                \
     hipError_t launch_##NAME(const ConvArgs &a, hipStream_t s) {                     \
         if (a.bf16)                                                                  \
-            return conv_vec<BF16>(a, BWD) ? NAME##_io<BF16, BWD ? 4 : 8>(a, s) : NAME##_io<BF16, 1>(a, s); \
+            return conv_vec<BF16>(a, BWD) ? NAME##_io<BF16, 4>(a, s) : NAME##_io<BF16, 1>(a, s); \
         return conv_vec<F32>(a, BWD) ? NAME##_io<F32, 4>(a, s) : NAME##_io<F32, 1>(a, s); \
     }
 CONV_BY_WIDTH(conv_fwd, false)

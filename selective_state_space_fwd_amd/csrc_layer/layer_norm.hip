@@ -26,6 +26,40 @@ __device__ __forceinline__ uint32_t pack8(float a, float b, float c, float d) {
     return __builtin_amdgcn_cvt_pk_fp8_f32(clamp8(c), clamp8(d), v, true);
 }
 
+// A block's scale and its values, for its largest magnitude m.  A block of
+// zeros (or below 2^-100, where 448 / m overflows) has scale 0.
+__device__ __forceinline__ float scale8(float m) { return m < 0x1p-100f ? 0.0f : m / 448.0f; }
+template <int VW>
+__device__ __forceinline__ void store8(uint8_t *q, const float (&v)[VW], float m) {
+    const float inv = m < 0x1p-100f ? 0.0f : 448.0f / m;
+    if constexpr (VW == 1) {
+        *q = static_cast<uint8_t>(pack8(v[0] * inv, 0.0f, 0.0f, 0.0f));
+    } else {
+        uint32_t o[VW / 4];
+#pragma unroll
+        for (int i = 0; i < VW; i += 4)
+            o[i / 4] = pack8(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+        __builtin_memcpy(__builtin_assume_aligned(q, VW), o, VW);
+    }
+}
+
+// The largest magnitude, as bits: those of non-negative floats order as the
+// floats do, NaN above all.
+template <int VW>
+__device__ __forceinline__ uint32_t vec_max(const float (&v)[VW]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+}
+// Over the 16 lanes of a row, in all of them.
+__device__ __forceinline__ uint32_t row_max(uint32_t m) {
+    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, m, 0x121, 0xf, 0xf, false)));
+    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, m, 0x122, 0xf, 0xf, false)));
+    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, m, 0x124, 0xf, 0xf, false)));
+    return max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, m, 0x128, 0xf, 0xf, false)));
+}
+
 template <class IO, class RT, int VW, int NV>
 __global__ __launch_bounds__(512) void norm_fwd_kernel(NormArgs a) {
     using T = typename IO::T;
@@ -36,9 +70,10 @@ __global__ __launch_bounds__(512) void norm_fwd_kernel(NormArgs a) {
     const int64_t ng = a.d / a.group;
     const int64_t row = blockIdx.x / ng, g0 = (blockIdx.x % ng) * a.group;
     const int nblk = a.block ? static_cast<int>((a.group + a.block - 1) / a.block) : 0;
+    const bool lanes = VW > 1 && a.block == 16 * VW;    // a block is a row of 16 lanes
     for (int i = tid; i < nblk; i += blockDim.x) most[i] = 0;
 
-    float v[NV][VW];
+    float v[NV][VW], wt[NV][VW];
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -48,6 +83,7 @@ __global__ __launch_bounds__(512) void norm_fwd_kernel(NormArgs a) {
         if (e < a.group) {
             const int64_t c = g0 + e;
             load_vec<IO, VW>(static_cast<const T *>(a.x) + row * a.x_row + c, v[k]);
+            load_vec<F32, VW>(a.weight + c, wt[k]);     // on its way before the sum is known
             if (a.residual) {
                 float r[VW];
                 load_vec<RT, VW>(static_cast<const typename RT::T *>(a.residual) + row * a.res_row + c, r);
@@ -89,50 +125,38 @@ __global__ __launch_bounds__(512) void norm_fwd_kernel(NormArgs a) {
     for (int k = 0; k < NV; ++k) {
         const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
         if (e < a.group) {
-            float w[VW];
-            load_vec<F32, VW>(a.weight + g0 + e, w);
 #pragma unroll
-            for (int i = 0; i < VW; ++i) v[k][i] = v[k][i] * rs * w[i];
+            for (int i = 0; i < VW; ++i) v[k][i] = v[k][i] * rs * wt[k][i];
             if (!nblk) {
                 store_vec<IO, VW>(static_cast<T *>(a.y) + row * a.d + g0 + e, v[k]);
-            } else {
-                // bits of non-negative floats order as the floats do, NaN above all
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < VW; ++i) {
-                    const uint32_t b = __float_as_uint(v[k][i]) & 0x7fffffffu;
-                    m = b > m ? b : m;
-                }
-                atomicMax(most + e / a.block, m);   // a maximum: no order changes it
+            } else if (!lanes) {
+                atomicMax(most + e / a.block, vec_max<VW>(v[k]));   // no order changes a maximum
             }
         }
     }
     if (!nblk) return;
+    if (lanes) {
+        uint8_t *q = static_cast<uint8_t *>(a.y) + row * a.d + g0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+            const uint32_t m = row_max(vec_max<VW>(v[k]));
+            if (e >= a.group) continue;
+            store8<VW>(q + e, v[k], __uint_as_float(m));
+            if ((tid & 15) == 0)
+                a.scale[(row * ng + g0 / a.group) * nblk + e / a.block] = scale8(__uint_as_float(m));
+        }
+        return;
+    }
     __syncthreads();
     uint8_t *q = static_cast<uint8_t *>(a.y) + row * a.d + g0;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
-        if (e < a.group) {
-            // a block of zeros (or below 2^-100, where 448 / max overflows) has scale 0
-            const float m = __uint_as_float(most[e / a.block]);
-            const float inv = m < 0x1p-100f ? 0.0f : 448.0f / m;
-            if constexpr (VW == 1) {
-                q[e] = static_cast<uint8_t>(pack8(v[k][0] * inv, 0.0f, 0.0f, 0.0f));
-            } else {
-                uint32_t o[VW / 4];
-#pragma unroll
-                for (int i = 0; i < VW; i += 4)
-                    o[i / 4] = pack8(v[k][i] * inv, v[k][i + 1] * inv, v[k][i + 2] * inv,
-                                     v[k][i + 3] * inv);
-                if constexpr (VW == 8) *reinterpret_cast<uint2 *>(q + e) = make_uint2(o[0], o[1]);
-                else *reinterpret_cast<uint32_t *>(q + e) = o[0];
-            }
-        }
+        if (e < a.group) store8<VW>(q + e, v[k], __uint_as_float(most[e / a.block]));
     }
     for (int i = tid; i < nblk; i += blockDim.x) {
-        const float m = __uint_as_float(most[i]);
-        a.scale[(row * ng + g0 / a.group) * nblk + i] = m < 0x1p-100f ? 0.0f : m / 448.0f;
+        a.scale[(row * ng + g0 / a.group) * nblk + i] = scale8(__uint_as_float(most[i]));
     }
 }
 
