@@ -482,9 +482,10 @@ struct ChunkMem {
     __attribute__((aligned(16))) E U[Q * LU];
     __attribute__((aligned(16))) E Y[Q * LU];
     __attribute__((aligned(16))) typename M::Half Mh[TRI * 64];
-    // a head's tokens: exp(s), exp(s_Q - s), exp(s - r), s - r and dt with r the
-    // sum before the token's tile; exp(r_q - s) for the tiles q behind it
-    __attribute__((aligned(16))) float tok[5 * Q + TT * (TT - 1) / 2 * 16];
+    // a head's tokens: exp(s), exp(s_Q - s), exp(s - r), s - r (in two floats) and
+    // dt with r the sum before the token's tile; exp(r_q - s) for the tiles q
+    // behind it
+    __attribute__((aligned(16))) float tok[6 * Q + TT * (TT - 1) / 2 * 16];
 };
 
 // What a chunk and head leave for heads_grad_kernel: row and column sums of Z
@@ -645,7 +646,7 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         for (int n = 0; n < NW; ++n) dB[q][n] = dC[q][n] = zero;
     __syncthreads();                            // C gives its place to h
 
-    float *es = mem.tok, *we = es + Q, *rt = es + 2 * Q, *sd = es + 3 * Q, *dts = es + 4 * Q, *cx = es + 5 * Q;
+    float *es = mem.tok, *we = es + Q, *rt = es + 2 * Q, *sd = es + 3 * Q, *dts = es + 5 * Q, *cx = es + 6 * Q;
     float xdot = 0.0f;
     int h = h0, p0 = 0;
     while (h < h1) {
@@ -707,6 +708,7 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
                 for (int q = 1; q < TT; ++q) own = g == q ? ref[q] : own;
                 rt[lane] = exp2_d(s - own);
                 sd[lane] = static_cast<float>(s - own);
+                sd[Q + lane] = static_cast<float>(s - own - sd[lane]);
             }
             if (wv == 3) {
 #pragma unroll
@@ -737,10 +739,12 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
             if (r < q) {
                 d = *reinterpret_cast<const f4 *>(rt + 16 * q + 4 * g) * cx[q * (q - 1) / 2 * 16 + 16 * r + l];
             } else {
-                const float x = sd[16 * r + l];
+                const float x = sd[16 * r + l], xl = sd[Q + 16 * r + l];
                 const f4 y = *reinterpret_cast<const f4 *>(sd + 16 * q + 4 * g);
+                const f4 yl = *reinterpret_cast<const f4 *>(sd + Q + 16 * q + 4 * g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] = l <= 4 * g + i ? exp2_hw(y[i] - x) : 0.0f;
+                for (int i = 0; i < 4; ++i)
+                    d[i] = l <= 4 * g + i ? exp2_hw((y[i] - x) + (yl[i] - xl)) : 0.0f;
             }
             if (p0 == 0) mem.Mh[idx * 64 + lane] = M::half(CB[o] * d);
             if (last) {

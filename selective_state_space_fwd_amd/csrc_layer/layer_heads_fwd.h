@@ -49,13 +49,14 @@ struct FwdMem {
     static constexpr int LC = NP + M::kPad, LU = 64 + M::kPad;
     static constexpr int LB = NP + (sizeof(E) == 2 ? 16 : M::kPad);
     static constexpr int TT = Q / 16, TRI = TT * (TT + 1) / 2;
-    static constexpr int kTok = FULL ? 5 * Q + TT * (TT - 1) / 2 * 16 : Q;
+    static constexpr int kTok = FULL ? 6 * Q + TT * (TT - 1) / 2 * 16 : Q;
     __attribute__((aligned(16))) E B[Q * LB];
     __attribute__((aligned(16))) E C[FULL ? Q * LC : 8];
     __attribute__((aligned(16))) E U[Q * LU];
     __attribute__((aligned(16))) typename M::Half Mh[FULL ? HW * TRI * 64 : 1];
-    // a head's tokens: dt exp(s_Q - s); exp(s); exp(s - r), s - r and dt with r
-    // the sum before the token's tile; dt exp(r_j - s) for the tiles j behind it
+    // a head's tokens: dt exp(s_Q - s); exp(s); exp(s - r), s - r (in two floats:
+    // differences of it count) and dt with r the sum before the token's tile;
+    // dt exp(r_j - s) for the tiles j behind it
     __attribute__((aligned(16))) float tok[HW][kTok];
 };
 
@@ -118,8 +119,8 @@ __global__ __launch_bounds__(256, (fwd_waves<IO, NP, HW, Q, FULL>())) void heads
     const int nh = HW == 1 ? 1 : head_slot(3) + 1;
     const double A2 = static_cast<double>(a.A[h]) * 1.4426950408889634;
     const float Dh = FULL && a.D ? a.D[h] : 0.0f, bias = a.bias ? a.bias[h] : 0.0f;
-    float *ws = mem.tok[hs], *es = ws + Q, *rt = ws + 2 * Q, *sd = ws + 3 * Q, *dts = ws + 4 * Q,
-          *cd = ws + 5 * Q;
+    float *ws = mem.tok[hs], *es = ws + Q, *rt = ws + 2 * Q, *sd = ws + 3 * Q, *dts = ws + 5 * Q,
+          *cd = ws + 6 * Q;
 
     f4 S[NT];                                   // state: rows n, columns p
     // a head's state of (rows, H, P, N), through a view: 16 bytes at a time
@@ -295,6 +296,7 @@ __global__ __launch_bounds__(256, (fwd_waves<IO, NP, HW, Q, FULL>())) void heads
                     for (int q = 1; q < TT; ++q) own = g == q ? ref[q] : own;
                     rt[lane] = exp2_d(s - own);
                     sd[lane] = static_cast<float>(s - own);
+                    sd[Q + lane] = static_cast<float>(s - own - sd[lane]);
                     dts[lane] = dt;
                 }
                 if (rank == mates - 1) {
@@ -358,15 +360,16 @@ __global__ __launch_bounds__(256, (fwd_waves<IO, NP, HW, Q, FULL>())) void heads
                     f4 v;
                     if (r < q) {
                         v = T[o] * *reinterpret_cast<const f4 *>(
-                                       tk + 5 * Q + q * (q - 1) / 2 * 16 + 16 * r + 4 * g);
+                                       tk + 6 * Q + q * (q - 1) / 2 * 16 + 16 * r + 4 * g);
                         v *= tk[2 * Q + 16 * q + l];
                     } else {
-                        const float y = tk[3 * Q + 16 * q + l];
+                        const float y = tk[3 * Q + 16 * q + l], yl = tk[4 * Q + 16 * q + l];
                         const f4 z = *reinterpret_cast<const f4 *>(tk + 3 * Q + 16 * r + 4 * g);
-                        const f4 d = *reinterpret_cast<const f4 *>(tk + 4 * Q + 16 * r + 4 * g);
+                        const f4 zl = *reinterpret_cast<const f4 *>(tk + 4 * Q + 16 * r + 4 * g);
+                        const f4 d = *reinterpret_cast<const f4 *>(tk + 5 * Q + 16 * r + 4 * g);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[i] = 4 * g + i <= l ? T[o][i] * (exp2_hw(y - z[i]) * d[i]) : 0.0f;
+                            v[i] = 4 * g + i <= l ? T[o][i] * (exp2_hw((y - z[i]) + (yl - zl[i])) * d[i]) : 0.0f;
                     }
                     mem.Mh[((HW == 1 ? 0 : x) * Mem::TRI + q * (q + 1) / 2 + r) * 64 + lane] = M::half(v);
                 }
