@@ -71,8 +71,18 @@ def declare(lib):
         fn.argtypes, fn.restype = args, res
 
 
-from . import (PreparedCall, _check, _expect, _io_code, _ptr, _stream, _torch,  # noqa: E402
-               load_library)
+from . import PreparedCall, _check, _io_code, load_library  # noqa: E402
+
+_torch = None
+
+
+def _t():
+    """torch, imported by the first call."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 class _LayerCall(PreparedCall):
@@ -83,7 +93,7 @@ class _LayerCall(PreparedCall):
     def __call__(self, profile_events=None, stream=None):
         if profile_events is not None:
             raise ValueError("the layer entry points record no events")
-        cuda = _torch().cuda
+        cuda = _t().cuda
         if self._device.index == cuda.current_device():
             return super().__call__(None, stream)
         with cuda.device(self._device):
@@ -91,42 +101,63 @@ class _LayerCall(PreparedCall):
 
 
 def _issue(prepare, fn, desc, args, keep, result, device):
-    args = args + (_stream(device),)
-    cuda = _torch().cuda
+    cuda = _t().cuda
+    stream = cuda.current_stream(device).cuda_stream
     if prepare:
-        call = _LayerCall(fn, desc, args, keep, result)
+        call = _LayerCall(fn, desc, args + (stream,), keep, result)
         call._device = device
         return call
     if device.index == cuda.current_device():
-        _check(fn(ctypes.byref(desc), *args))
+        status = fn(ctypes.byref(desc), *args, stream)
     else:
         with cuda.device(device):
-            _check(fn(ctypes.byref(desc), *args))
+            status = fn(ctypes.byref(desc), *args, stream)
+    if status:
+        _check(status)
     return result
 
 
-def _rows(t, name, shape, dtype, device, inner):
-    """Checks an activation whose last `inner` dimensions lie side by side, as
-    columns of rows any distance apart; returns its leading strides."""
-    if tuple(t.shape) != tuple(shape):
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _like(t, name, shape, dtype, device):
+    """Checks a shape (a tuple), a type and a device."""
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    st, want = t.stride(), 1
-    for i in range(len(shape) - 1, len(shape) - 1 - inner, -1):
-        if shape[i] != 1 and st[i] != want:
+
+
+def _expect(t, name, shape, dtype, device):
+    if t is None:
+        return
+    _like(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name, shape, dtype, device, inner):
+    """Checks an activation whose last `inner` dimensions lie side by side, as
+    columns of rows any distance apart; returns its leading strides."""
+    _like(t, name, shape, dtype, device)
+    st, want, n = t.stride(), 1, len(shape)
+    for i in range(n - 1, n - 1 - inner, -1):
+        if st[i] != want and shape[i] != 1:
             raise ValueError(f"{name}: the last {inner} dimension(s) must be contiguous")
         want *= shape[i]
     # the distance between rows of which there is one does not matter
-    return [0 if shape[i] == 1 else st[i] for i in range(len(shape) - inner)]
+    lead = st[:n - inner]
+    return lead if 1 not in shape[:n - inner] else tuple(
+        0 if shape[i] == 1 else lead[i] for i in range(n - inner))
 
 
 def _offsets(cu_seqlens, batch, device):
     if cu_seqlens is None:
         return 0, batch
-    torch = _torch()
+    torch = _t()
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must hold n_seqs + 1 >= 2 offsets")
     n = cu_seqlens.numel() - 1
@@ -140,7 +171,7 @@ def _room(need, workspace, desc, device):
     if need == 0:
         return None
     if workspace is None:
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+        workspace = _t().empty(need, dtype=_t().uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous memory on {device}")
     desc.workspace = workspace.data_ptr()
@@ -159,7 +190,7 @@ def _cuda(t, name):
 def _heads_desc(u, delta, A, B, C, D, delta_bias, softplus, tokens):
     """Checks what every form of the scan over heads takes; tokens: whether a
     token dimension follows the batch's."""
-    torch = _torch()
+    torch = _t()
     if u.dim() != 3 + tokens:
         raise ValueError(f"u: expected {3 + tokens} dimensions, got {tuple(u.shape)}")
     if B.dim() != 3 + tokens:
@@ -168,22 +199,19 @@ def _heads_desc(u, delta, A, B, C, D, delta_bias, softplus, tokens):
     H, P = u.shape[-2:]
     G, N = B.shape[-2:]
     dev, io = _cuda(u, "u"), u.dtype
-    desc = HeadsDesc(batch=lead[0], seqlen=lead[1] if tokens else 1, heads=H, head_dim=P,
-                     groups=G, d_state=N, io_dtype=_io_code(io), softplus=int(bool(softplus)))
-
-    def put(name, st):
-        setattr(desc, name + "_batch_stride", st[0])
-        if tokens:
-            setattr(desc, name + "_token_stride", st[1])
-
-    put("u", _rows(u, "u", lead + (H, P), io, dev, 2))
-    put("delta", _rows(delta, "delta", lead + (H,), io, dev, 1))
-    put("B", _rows(B, "B", lead + (G, N), io, dev, 2))
-    put("C", _rows(C, "C", lead + (G, N), io, dev, 2))
-    _expect(A, "A", (H,), torch.float32, dev)
-    _expect(D, "D", (H,), torch.float32, dev)
-    _expect(delta_bias, "delta_bias", (H,), torch.float32, dev)
-    return desc, dev, io, lead, put
+    us = _rows(u, "u", lead + (H, P), io, dev, 2)
+    ds = _rows(delta, "delta", lead + (H,), io, dev, 1)
+    bs = _rows(B, "B", lead + (G, N), io, dev, 2)
+    cs = _rows(C, "C", lead + (G, N), io, dev, 2)
+    f32 = torch.float32
+    _expect(A, "A", (H,), f32, dev)
+    _expect(D, "D", (H,), f32, dev)
+    _expect(delta_bias, "delta_bias", (H,), f32, dev)
+    if not tokens:
+        us, ds, bs, cs = us + (0,), ds + (0,), bs + (0,), cs + (0,)
+    desc = HeadsDesc(lead[0], lead[1] if tokens else 1, H, P, G, N, 0, us[0], us[1], ds[0], ds[1],
+                     bs[0], bs[1], cs[0], cs[1], 0, 0, _io_code(io), 1 if softplus else 0)
+    return desc, dev, io, lead
 
 
 def ssm_heads_fwd(u, delta, A, B, C, D=None, delta_bias=None, softplus=True,
@@ -201,14 +229,14 @@ def ssm_heads_fwd(u, delta, A, B, C, D=None, delta_bias=None, softplus=True,
     prepare: check and marshal only, return a PreparedCall.
     Returns (y, last_state); last_state is None unless requested.
     """
-    torch = _torch()
+    torch = _t()
     lib = load_library()
-    desc, dev, io, lead, _ = _heads_desc(u, delta, A, B, C, D, delta_bias, softplus, 1)
+    desc, dev, io, lead = _heads_desc(u, delta, A, B, C, D, delta_bias, softplus, 1)
     desc.n_seqs, rows = _offsets(cu_seqlens, lead[0], dev)
     state = (rows, desc.heads, desc.head_dim, desc.d_state)
     _expect(initial_state, "initial_state", state, torch.float32, dev)
     if y is None:
-        y = torch.empty(u.shape, dtype=io, device=dev)
+        y = u.new_empty(u.shape)
     _expect(y, "y", u.shape, io, dev)
     if last_state is None and return_last_state:
         last_state = torch.empty(state, dtype=torch.float32, device=dev)
@@ -230,10 +258,10 @@ def ssm_heads_bwd(u, delta, A, B, C, dy, D=None, delta_bias=None, softplus=True,
     without initial_state) float32.  Nothing of the forward call is needed;
     other arguments as there.
     """
-    torch = _torch()
+    torch = _t()
     lib = load_library()
-    desc, dev, io, lead, put = _heads_desc(u, delta, A, B, C, D, delta_bias, softplus, 1)
-    put("dy", _rows(dy, "dy", tuple(u.shape), io, dev, 2))
+    desc, dev, io, lead = _heads_desc(u, delta, A, B, C, D, delta_bias, softplus, 1)
+    desc.dy_batch_stride, desc.dy_token_stride = _rows(dy, "dy", tuple(u.shape), io, dev, 2)
     desc.n_seqs, rows = _offsets(cu_seqlens, lead[0], dev)
     state = (rows, desc.heads, desc.head_dim, desc.d_state)
     _expect(initial_state, "initial_state", state, torch.float32, dev)
@@ -257,7 +285,7 @@ def ssm_heads_bwd(u, delta, A, B, C, dy, D=None, delta_bias=None, softplus=True,
 
 
 def _slots(slots, batch, n_slots, dev):
-    _expect(slots, "slots", (batch,), _torch().int32, dev)
+    _expect(slots, "slots", (batch,), _t().int32, dev)
     if slots is None and batch > n_slots:
         raise ValueError(f"{batch} rows, but {n_slots} states")
 
@@ -272,14 +300,14 @@ def ssm_heads_update(state, u, delta, A, B, C, D=None, delta_bias=None, softplus
     i); a row whose slot lies outside 0 .. n_slots - 1 is skipped, its y left
     as it was; slots of one call must differ.  Returns y (rows, heads, head_dim).
     """
-    torch = _torch()
+    torch = _t()
     lib = load_library()
-    desc, dev, io, lead, _ = _heads_desc(u, delta, A, B, C, D, delta_bias, softplus, 0)
+    desc, dev, io, lead = _heads_desc(u, delta, A, B, C, D, delta_bias, softplus, 0)
     n = state.shape[0]
     _expect(state, "state", (n, desc.heads, desc.head_dim, desc.d_state), torch.float32, dev)
     _slots(slots, lead[0], n, dev)
     if y is None:
-        y = torch.empty(u.shape, dtype=io, device=dev)
+        y = u.new_empty(u.shape)
     _expect(y, "y", u.shape, io, dev)
     args = (_ptr(state), _ptr(slots), n) + tuple(map(_ptr, (u, delta, A, B, C, D, delta_bias, y)))
     keep = (state, slots, u, delta, A, B, C, D, delta_bias)
@@ -289,7 +317,7 @@ def ssm_heads_update(state, u, delta, A, B, C, D=None, delta_bias=None, softplus
 # --------------------------------------------------------------- convolution
 
 def _conv_desc(x, weight, bias, silu, tokens):
-    torch = _torch()
+    torch = _t()
     if x.dim() != 2 + tokens:
         raise ValueError(f"x: expected {2 + tokens} dimensions, got {tuple(x.shape)}")
     ch = x.shape[-1]
@@ -297,9 +325,8 @@ def _conv_desc(x, weight, bias, silu, tokens):
         raise ValueError(f"weight must be (channels, width), got {tuple(weight.shape)}")
     dev, io, W = _cuda(x, "x"), x.dtype, weight.shape[1]
     st = _rows(x, "x", tuple(x.shape), io, dev, 1)
-    desc = ConvDesc(batch=x.shape[0], seqlen=x.shape[1] if tokens else 1, channels=ch, width=W,
-                    io_dtype=_io_code(io), silu=int(bool(silu)), x_batch_stride=st[0],
-                    x_token_stride=st[1] if tokens else 0)
+    desc = ConvDesc(x.shape[0], x.shape[1] if tokens else 1, ch, 0, st[0], st[1] if tokens else 0,
+                    0, 0, W, _io_code(io), 1 if silu else 0)
     _expect(weight, "weight", (ch, W), torch.float32, dev)
     _expect(bias, "bias", (ch,), torch.float32, dev)
     return desc, dev, io
@@ -315,14 +342,14 @@ def ssm_conv_fwd(x, weight, bias=None, silu=True, conv_state=None, cu_seqlens=No
     zeros; cu_seqlens as in ssm_heads_fwd.  Returns (y, last_state), the latter
     the conv_state behind each sequence (None unless requested).
     """
-    torch = _torch()
+    torch = _t()
     lib = load_library()
     desc, dev, io = _conv_desc(x, weight, bias, silu, 1)
     desc.n_seqs, rows = _offsets(cu_seqlens, desc.batch, dev)
     state = (rows, desc.channels, desc.width - 1)
     _expect(conv_state, "conv_state", state, torch.float32, dev)
     if y is None:
-        y = torch.empty(x.shape, dtype=io, device=dev)
+        y = x.new_empty(x.shape)
     _expect(y, "y", x.shape, io, dev)
     if last_state is None and return_last_state:
         last_state = torch.empty(state, dtype=torch.float32, device=dev)
@@ -337,7 +364,7 @@ def ssm_conv_bwd(x, weight, dy, bias=None, silu=True, conv_state=None, cu_seqlen
     """Gradients of sum(dy * y) of ssm_conv_fwd: a dict of dx (in x's type) and
     float32 dweight, dbias (None without bias), dconv_state (None without
     conv_state)."""
-    torch = _torch()
+    torch = _t()
     lib = load_library()
     desc, dev, io = _conv_desc(x, weight, bias, silu, 1)
     desc.dy_batch_stride, desc.dy_token_stride = _rows(dy, "dy", tuple(x.shape), io, dev, 1)
@@ -362,14 +389,14 @@ def ssm_conv_update(conv_state, x, weight, bias=None, silu=True, slots=None, y=N
     """One token of the convolution: x (rows, channels); conv_state (n_slots,
     channels, W - 1) float32 moves on by one in place; slots as in
     ssm_heads_update.  Returns y (rows, channels)."""
-    torch = _torch()
+    torch = _t()
     lib = load_library()
     desc, dev, io = _conv_desc(x, weight, bias, silu, 0)
     n = conv_state.shape[0]
     _expect(conv_state, "conv_state", (n, desc.channels, desc.width - 1), torch.float32, dev)
     _slots(slots, desc.batch, n, dev)
     if y is None:
-        y = torch.empty(x.shape, dtype=io, device=dev)
+        y = x.new_empty(x.shape)
     _expect(y, "y", x.shape, io, dev)
     args = (_ptr(conv_state), _ptr(slots), n) + tuple(map(_ptr, (x, weight, bias, y)))
     keep = (conv_state, slots, x, weight, bias)
@@ -379,7 +406,7 @@ def ssm_conv_update(conv_state, x, weight, bias=None, silu=True, slots=None, y=N
 # ---------------------------------------------------------------------- norm
 
 def _norm_desc(x, weight, io, res, group_size, eps):
-    torch = _torch()
+    torch = _t()
     if x.dim() != 2:
         raise ValueError(f"x: expected (rows, d), got {tuple(x.shape)}")
     rows, d = x.shape
@@ -387,9 +414,8 @@ def _norm_desc(x, weight, io, res, group_size, eps):
     group_size = group_size or d
     if group_size < 0 or d % group_size:
         raise ValueError(f"group_size {group_size} does not divide {d}")
-    desc = NormDesc(rows=rows, d=d, group_size=group_size, io_dtype=_io_code(io),
-                    residual_dtype=_io_code(res), eps=eps,
-                    x_stride=_rows(x, "x", (rows, d), x.dtype, dev, 1)[0])
+    xs = _rows(x, "x", (rows, d), x.dtype, dev, 1)[0]
+    desc = NormDesc(rows, d, group_size, 0, xs, 0, 0, 0, _io_code(io), _io_code(res), eps)
     _expect(weight, "weight", (d,), torch.float32, dev)
     return desc, dev
 
@@ -407,7 +433,7 @@ def ssm_norm_fwd(x, weight, residual=None, z=None, eps=1e-5, group_size=0, quant
     residual.  Returns (y, scale, s): scale None without quant_block, s (in the
     residual's type) None without residual.
     """
-    torch = _torch()
+    torch = _t()
     lib = load_library()
     desc, dev = _norm_desc(x, weight, x.dtype, x.dtype if residual is None else residual.dtype,
                            group_size, eps)
@@ -447,7 +473,7 @@ def ssm_norm_bwd(x, weight, dy, z=None, dresidual=None, eps=1e-5, group_size=0, 
     dict: dx (the gradient of x and of the residual alike, in x's type), dz
     (None without z, in dy's), dweight float32.
     """
-    torch = _torch()
+    torch = _t()
     lib = load_library()
     desc, dev = _norm_desc(x, weight, dy.dtype, x.dtype, group_size, eps)
     shape, io = tuple(x.shape), dy.dtype
