@@ -493,23 +493,15 @@ struct ChunkMem {
 template <int Q>
 struct GradRec {
     static constexpr int TT = Q / 16, TRI = TT * (TT + 1) / 2;
-    float rowz[TRI * 16], colv[TRI * 16], diag[Q], diagz[Q], xdot[4];
+    float rowz[TRI * 16], colv[TRI * 16], diag[Q], diagz[Q], xdot[8];
 };
 
-// Which tiles (q, r) of a triangle wavefront w has, o = 0, 1, ...; r < 0: none.
-template <int TT>
-__device__ __forceinline__ constexpr int own_q(int w, int o) {
-    if constexpr (TT == 2) return w == 0 ? 0 : 1;
-    return w == 3 ? (o == 0 ? 0 : 3) : 3 - w;
-}
-template <int TT>
-__device__ __forceinline__ constexpr int own_r(int w, int o) {
-    if constexpr (TT == 2) return o == 0 && w < 3 ? (w == 2 ? 1 : 0) : -1;
-    return w == 3 ? (o == 0 ? 0 : o == 1 ? 3 : -1) : o <= (w == 2 ? 1 : 2) ? o : -1;
-}
+// The row and column of tile i of a triangle's, in order of rows.
+__device__ __forceinline__ int tile_q(int i) { return (i >= 1) + (i >= 3) + (i >= 6); }
+__device__ __forceinline__ int tile_r(int i) { return i - tile_q(i) * (tile_q(i) + 1) / 2; }
 
 template <class IO, int NP, int Q, int PS, bool WIDE>
-__global__ __launch_bounds__(256, (sizeof(ChunkMem<IO, NP, Q, PS>) <= 80 * 1024 ? 2 : 1)) void
+__global__ __launch_bounds__(512, (sizeof(ChunkMem<IO, NP, Q, PS>) <= 80 * 1024 ? 4 : 2)) void
 heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     using M = Mat<IO>;
     using E = typename M::E;
@@ -520,9 +512,14 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     constexpr int V = Seg<IO>::VW, ES = sizeof(E);
     constexpr int NT = NP / 16, KN = NP / 32, TT = Q / 16, KS = Q / 32, KP = PS / 32;
     constexpr int LB = Mem::LB, LU = Mem::LU, LW = Mem::LW;
-    constexpr int OWN = TT == 2 ? 1 : 3, NW = (NT + 3) / 4, FOUR = M::pos(4);
-    constexpr int PU = PS / V, NU = Q * PU / 256, NS = PS * NP / V / 256;    // pieces of u (dy), h (gh)
-    static_assert(Q * PU % 256 == 0 && PS * NP / V % 256 == 0, "whole rounds of the workgroup");
+    constexpr int TRI = Mem::TRI, OWN = (TRI + 7) / 8, FOUR = M::pos(4);
+    // dB and dC: NW column tiles and QR row tiles a wavefront
+    constexpr int NW = NT > 8 ? NT / 8 : 1, QS = NT < 8 ? 8 / NT : 1, QR = TT > QS ? TT / QS : 1;
+    // du: 16 channels and RR row tiles a wavefront
+    constexpr int PT = PS / 16, RR = TT * PT > 8 ? TT * PT / 8 : 1;
+    static_assert(RR <= 2, "of one operand");
+    constexpr int PU = PS / V, TU = Q * PU, NU = (TU + 511) / 512;      // pieces of u (dy)
+    constexpr int TS = PS * NP / V, NS = (TS + 511) / 512;              // pieces of h (gh)
     extern __shared__ __attribute__((aligned(16))) unsigned char raw[];
     Mem &mem = *reinterpret_cast<Mem *>(raw);
 
@@ -549,14 +546,14 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
 
     auto put_bc = [&](E *to, const E *from, int64_t stride) {
         if constexpr (WIDE) {
-            for (int i = tid; i < Q * NP / V; i += 256) {
+            for (int i = tid; i < Q * NP / V; i += 512) {
                 const int t = i / (NP / V), c = i % (NP / V) * V;
                 u4 v = {0, 0, 0, 0};
                 if (t < k.n && c < N) v = *reinterpret_cast<const u4 *>(from + t * stride + c);
                 M::put_perm(to + t * LB, c, v);
             }
         } else {
-            for (int i = tid; i < Q * NP; i += 256) {
+            for (int i = tid; i < Q * NP; i += 512) {
                 const int t = i / NP, c = i % NP;
                 to[t * LB + M::pos(c)] = t < k.n && c < N ? from[t * stride + c] : E(0);
             }
@@ -578,11 +575,11 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
             const bool in = p0 + tid % PU * V < P;
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                const bool ok = in && tid / PU + i * (256 / PU) < k.n;
+                const bool ok = in && tid / PU + i * (512 / PU) < k.n;
                 Ur[i] = __builtin_amdgcn_raw_buffer_load_b128(ru, ok ? uo : kDrop,
-                                                              i * (256 / PU) * static_cast<int>(a.u_t) * ES, 0);
+                                                              i * (512 / PU) * static_cast<int>(a.u_t) * ES, 0);
                 Yr[i] = __builtin_amdgcn_raw_buffer_load_b128(ry, ok ? yo : kDrop,
-                                                              i * (256 / PU) * static_cast<int>(a.dy_t) * ES, 0);
+                                                              i * (512 / PU) * static_cast<int>(a.dy_t) * ES, 0);
             }
         }
         dtr = 0.0f;
@@ -599,8 +596,8 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         const Rsrc rg = view(static_cast<const E *>(a.gout) + at, bytes);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            Hr[i] = __builtin_amdgcn_raw_buffer_load_b128(rh, (tid + 256 * i) * 16, 0, 0);
-            Gr[i] = __builtin_amdgcn_raw_buffer_load_b128(rg, (tid + 256 * i) * 16, 0, 0);
+            Hr[i] = __builtin_amdgcn_raw_buffer_load_b128(rh, (tid + 512 * i) * 16, 0, 0);
+            Gr[i] = __builtin_amdgcn_raw_buffer_load_b128(rg, (tid + 512 * i) * 16, 0, 0);
         }
     };
     // a piece of a state, as the walks' lanes left it, into rows of channels
@@ -617,36 +614,28 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     put_bc(mem.B, Bp, a.B_t);
     put_bc(mem.HC, Cp, a.C_t);
     __syncthreads();
-    f4 CB[OWN], W[OWN], DX[OWN], dB[TT][NW], dC[TT][NW];
+    f4 CB[OWN], W[OWN], DX[OWN], dB[QR][NW], dC[QR][NW];
     const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int o = 0; o < OWN; ++o) W[o] = CB[o] = DX[o] = zero;
-    // one version of the tiles' work a wavefront, its tiles known
-    auto by_wave = [&](auto f) {
-        if (wv == 0) f(Int<0>());
-        else if (wv == 1) f(Int<1>());
-        else if (wv == 2) f(Int<2>());
-        else f(Int<3>());
-    };
-    by_wave([&](auto w) {                       // C_t . B_s: rows t, columns s
 #pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            constexpr int WV = decltype(w)::value;
-            const int r = own_r<TT>(WV, o), q = own_q<TT>(WV, o);
-            if (r < 0) continue;
+    for (int o = 0; o < OWN; ++o) {             // C_t . B_s: rows t, columns s
+        const int idx = wv + 8 * o, q = tile_q(idx), r = tile_r(idx);
+        if (idx >= TRI) continue;
 #pragma unroll
-            for (int m = 0; m < KN; ++m)
-                CB[o] = M::mma(M::row_perm(mem.HC + (16 * q + l) * LB + 32 * m, g),
-                               M::row_perm(mem.B + (16 * r + l) * LB + 32 * m, g), CB[o]);
-        }
-    });
+        for (int m = 0; m < KN; ++m)
+            CB[o] = M::mma(M::row_perm(mem.HC + (16 * q + l) * LB + 32 * m, g),
+                           M::row_perm(mem.B + (16 * r + l) * LB + 32 * m, g), CB[o]);
+    }
 #pragma unroll
-    for (int q = 0; q < TT; ++q)
+    for (int q = 0; q < QR; ++q)
 #pragma unroll
         for (int n = 0; n < NW; ++n) dB[q][n] = dC[q][n] = zero;
     __syncthreads();                            // C gives its place to h
 
     float *es = mem.tok, *we = es + Q, *rt = es + 2 * Q, *sd = es + 3 * Q, *dts = es + 5 * Q, *cx = es + 6 * Q;
+    const int nt0 = NT > 8 ? NW * wv : wv % NT, q0 = NT < 8 ? wv / NT * QR : 0;
+    const int pc = 16 * (wv % PT), r0 = wv / PT * RR;
     float xdot = 0.0f;
     int h = h0, p0 = 0;
     while (h < h1) {
@@ -661,11 +650,12 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         if constexpr (WIDE) {
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                M::put_perm(mem.U + (tid / PU + i * (256 / PU)) * LU, tid % PU * V, Ur[i]);
-                M::put_perm(mem.Y + (tid / PU + i * (256 / PU)) * LU, tid % PU * V, Yr[i]);
+                if (TU % 512 != 0 && tid + 512 * i >= TU) continue;
+                M::put_perm(mem.U + (tid / PU + i * (512 / PU)) * LU, tid % PU * V, Ur[i]);
+                M::put_perm(mem.Y + (tid / PU + i * (512 / PU)) * LU, tid % PU * V, Yr[i]);
             }
         } else {
-            for (int i = tid; i < Q * PS; i += 256) {
+            for (int i = tid; i < Q * PS; i += 512) {
                 const int t = i / PS, c = i % PS;
                 const bool in = t < k.n && p0 + c < P;
                 mem.U[t * LU + M::pos(c)] = in ? Up[t * a.u_t + h * P + p0 + c] : E(0);
@@ -680,8 +670,9 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         const bool direct = ES == 4 || exp2_d(sQ) < kDirect;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            put_state(mem.HC, tid + 256 * i, Hr[i]);
-            put_state(mem.G, tid + 256 * i, Gr[i]);
+            if (TS % 512 != 0 && tid + 512 * i >= TS) continue;
+            put_state(mem.HC, tid + 512 * i, Hr[i]);
+            put_state(mem.G, tid + 512 * i, Gr[i]);
             if (direct) {
                 float x[V], y[V];
                 typename Seg<IO>::V hv, gv;
@@ -717,18 +708,17 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
             }
         }
         __syncthreads();
+        asm volatile("" : "+v"(l), "+v"(g), "+v"(lane));
         // ---- the wavefront's tiles: decayed products for v (k = t), dy_t . u_s
         GradRec<Q> *rc = rec + static_cast<int64_t>(ci) * H + h;
         if (p0 == 0) {
 #pragma unroll
             for (int o = 0; o < OWN; ++o) DX[o] = zero;
         }
-        by_wave([&](auto w) {
-        constexpr int WV = decltype(w)::value;
 #pragma unroll
         for (int o = 0; o < OWN; ++o) {
-            const int r = own_r<TT>(WV, o), q = own_q<TT>(WV, o), idx = q * (q + 1) / 2 + r;
-            if (r < 0) continue;
+            const int idx = wv + 8 * o, q = tile_q(idx), r = tile_r(idx);
+            if (idx >= TRI) continue;
 #pragma unroll
             for (int m = 0; m < KP; ++m)
                 DX[o] = M::mma(M::row_perm(mem.Y + (16 * q + l) * LU + 32 * m, g),
@@ -768,110 +758,119 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
                 if (l == 0) *reinterpret_cast<f4 *>(rc->rowz + idx * 16 + 4 * g) = row;
             }
         }
-        });
         if (last && direct) {
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) xdot += __shfl_xor(xdot, o, 64);
             if (lane == 0) rc->xdot[wv] = xdot;
         }
         if (last) xdot = 0.0f;
-        // ---- what the states give dC and dB: a quarter of the columns n a wavefront
-        if (NT >= 4 || wv < NT) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" : "+v"(l), "+v"(g), "+v"(lane));
+        // ---- what the states give dC and dB
+        if (q0 < TT) {
             Frag hf[NW][KP], gf[NW][KP];
 #pragma unroll
             for (int n = 0; n < NW; ++n)
 #pragma unroll
                 for (int m = 0; m < KP; ++m) {
-                    const int at = 32 * m * LB + M::pos(16 * n) + (NW == 1 ? M::pos(16 * wv) : 16 * NW * wv);
+                    const int at = 32 * m * LB + M::pos(16 * (nt0 + n));
                     hf[n][m] = M::template col_perm<FOUR>(mem.HC + at, LB, g, l);
                     gf[n][m] = M::template col_perm<FOUR>(mem.G + at, LB, g, l);
                 }
 #pragma unroll
-            for (int q = 0; q < TT; ++q) {
+            for (int q = 0; q < QR; ++q) {
                 f4 x[NW], y[NW];
 #pragma unroll
                 for (int n = 0; n < NW; ++n) x[n] = y[n] = zero;
 #pragma unroll
                 for (int m = 0; m < KP; ++m) {
-                    const Frag yr = M::row_perm(mem.Y + (16 * q + l) * LU + 32 * m, g);
-                    const Frag ur = M::row_perm(mem.U + (16 * q + l) * LU + 32 * m, g);
+                    const Frag yr = M::row_perm(mem.Y + (16 * (q0 + q) + l) * LU + 32 * m, g);
+                    const Frag ur = M::row_perm(mem.U + (16 * (q0 + q) + l) * LU + 32 * m, g);
 #pragma unroll
                     for (int n = 0; n < NW; ++n) {
                         x[n] = M::mma(yr, hf[n][m], x[n]);
                         y[n] = M::mma(ur, gf[n][m], y[n]);
                     }
                 }
-                const f4 e = *reinterpret_cast<const f4 *>(es + 16 * q + 4 * g);
-                const f4 w = *reinterpret_cast<const f4 *>(we + 16 * q + 4 * g) *
-                             *reinterpret_cast<const f4 *>(dts + 16 * q + 4 * g);
+                const f4 e = *reinterpret_cast<const f4 *>(es + 16 * (q0 + q) + 4 * g);
+                const f4 w = *reinterpret_cast<const f4 *>(we + 16 * (q0 + q) + 4 * g) *
+                             *reinterpret_cast<const f4 *>(dts + 16 * (q0 + q) + 4 * g);
 #pragma unroll
                 for (int n = 0; n < NW; ++n) {
                     dC[q][n] += e * x[n];
                     dB[q][n] += w * y[n];
+                    // added here, not where the loop ends, x and y kept until then
+                    asm volatile("" : "+v"(dC[q][n]), "+v"(dB[q][n]));
                 }
             }
         }
-        // ---- du of 16 channels a wavefront: first what gh gives
-        f4 X[TT];
-        if (16 * wv < PS) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" : "+v"(l), "+v"(g), "+v"(lane));
+        // ---- du: first what gh gives
+        f4 X[RR];
+        if (r0 < TT) {
 #pragma unroll
-            for (int r = 0; r < TT; ++r) X[r] = zero;
+            for (int r = 0; r < RR; ++r) X[r] = zero;
 #pragma unroll
             for (int m = 0; m < KN; ++m) {
-                const Frag gf = M::row_perm(mem.G + (16 * wv + l) * LB + 32 * m, g);
+                const Frag gf = M::row_perm(mem.G + (pc + l) * LB + 32 * m, g);
 #pragma unroll
-                for (int r = 0; r < TT; ++r)
-                    X[r] = M::mma(M::row_perm(mem.B + (16 * r + l) * LB + 32 * m, g), gf, X[r]);
+                for (int r = 0; r < RR; ++r)
+                    X[r] = M::mma(M::row_perm(mem.B + (16 * (r0 + r) + l) * LB + 32 * m, g), gf, X[r]);
             }
 #pragma unroll
-            for (int r = 0; r < TT; ++r) X[r] *= *reinterpret_cast<const f4 *>(we + 16 * r + 4 * g);
+            for (int r = 0; r < RR; ++r) X[r] *= *reinterpret_cast<const f4 *>(we + 16 * (r0 + r) + 4 * g);
         }
         __syncthreads();                        // Mh is there; nobody reads u any more
-        if (16 * wv < PS) {
-            E *Ud = mem.U + M::pos(16 * wv) + (l >> 2) * FOUR + (l & 3);   // du in u's place
-            Frag yf[KS];
+        asm volatile("" : "+v"(l), "+v"(g), "+v"(lane));
+        if (r0 < TT) {
+            E *Ud = mem.U + M::pos(pc) + (l >> 2) * FOUR + (l & 3);     // du in u's place
 #pragma unroll
             for (int m = 0; m < KS; ++m) {
-                yf[m] = M::template col_perm<FOUR>(mem.Y + 32 * m * LU + M::pos(16 * wv), LU, g, l);
+                const Frag yf = M::template col_perm<FOUR>(mem.Y + 32 * m * LU + M::pos(pc), LU, g, l);
 #pragma unroll
-                for (int r = 0; r < 2 * m + 2; ++r) {
-                    const int i1 = (2 * m + 1) * (2 * m + 2) / 2 + r, i0 = 2 * m * (2 * m + 1) / 2 + r;
-                    X[r] = M::mma(M::join(r <= 2 * m ? mem.Mh[i0 * 64 + lane] : M::none(),
-                                          mem.Mh[i1 * 64 + lane]), yf[m], X[r]);
+                for (int r = 0; r < RR; ++r) {
+                    const int i1 = (2 * m + 1) * (2 * m + 2) / 2 + r0 + r, i0 = 2 * m * (2 * m + 1) / 2 + r0 + r;
+                    if (r0 + r > 2 * m + 1) continue;
+                    Half first = M::none();
+                    if (r0 + r <= 2 * m) first = mem.Mh[i0 * 64 + lane];
+                    X[r] = M::mma(M::join(first, mem.Mh[i1 * 64 + lane]), yf, X[r]);
                 }
             }
+            // the operand's values are dy where X's rows and columns are: RR row
+            // tiles are of one operand
+            float y[8];
+            M::unpack(M::template col_perm<FOUR>(mem.Y + 32 * (r0 / 2) * LU + M::pos(pc), LU, g, l), y);
 #pragma unroll
-            for (int m = 0; m < KS; ++m) {
-                float y[8];         // the operand's values are dy where X's rows and columns are
-                M::unpack(yf[m], y);
+            for (int r = 0; r < RR; ++r) {
+                const f4 dq = *reinterpret_cast<const f4 *>(dts + 16 * (r0 + r) + 4 * g);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const f4 dq = *reinterpret_cast<const f4 *>(dts + 16 * (2 * m + e) + 4 * g);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        IO::store(Ud, (16 * (2 * m + e) + 4 * g + i) * LU,
-                                  __builtin_fmaf(dq[i], X[2 * m + e][i], Dh * y[4 * e + i]));
+                for (int i = 0; i < 4; ++i) {
+                    const float y0 = y[i], y1 = y[4 + i];
+                    IO::store(Ud, (16 * (r0 + r) + 4 * g + i) * LU,
+                              __builtin_fmaf(dq[i], X[r][i], Dh * ((r0 + r) & 1 ? y1 : y0)));
                 }
             }
             __builtin_amdgcn_wave_barrier();
-            E *dug = Dp + h * P + p0 + 16 * wv;
-            const int ds = H * P, left = P - p0 - 16 * wv;
+            E *dug = Dp + h * P + p0 + pc;
+            const int ds = H * P, left = P - p0 - pc;
             if constexpr (WIDE) {
                 constexpr int pieces = 16 / V;
                 const Rsrc rd = view(dug, 0x7fffffff);
                 const int c = lane % pieces * V;
 #pragma unroll
-                for (int i = 0; i < Q * pieces / 64; ++i) {
-                    const int t = lane / pieces + i * (64 / pieces);
-                    __builtin_amdgcn_raw_buffer_store_b128(
-                        M::template get_perm<u4>(mem.U + t * LU, 16 * wv + c), rd,
-                        t < k.n && c < left ? static_cast<uint32_t>(t * ds + c) * ES : kDrop, 0, 0);
+                for (int i = 0; i < (16 * RR * pieces + 63) / 64; ++i) {
+                    const int tr = lane / pieces + i * (64 / pieces), t = 16 * r0 + tr;
+                    if (16 * RR * pieces % 64 == 0 || tr < 16 * RR)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            M::template get_perm<u4>(mem.U + t * LU, pc + c), rd,
+                            t < k.n && c < left ? static_cast<uint32_t>(t * ds + c) * ES : kDrop, 0, 0);
                 }
             } else {
-                for (int i = lane; i < Q * 16; i += 64) {
-                    const int t = i >> 4, c = i & 15;
+                for (int i = lane; i < 16 * RR * 16; i += 64) {
+                    const int t = 16 * r0 + (i >> 4), c = i & 15;
                     if (t < k.n && c < left)
-                        dug[static_cast<int64_t>(t) * ds + c] = mem.U[t * LU + M::pos(16 * wv + c)];
+                        dug[static_cast<int64_t>(t) * ds + c] = mem.U[t * LU + M::pos(pc + c)];
                 }
             }
         }
@@ -881,40 +880,40 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     }
     // ---- W over all heads, rows t by columns s, nothing above the diagonal
     E *Ws = mem.G;
-    for (int i = tid; i < Q * LW; i += 256) Ws[i] = E(0);
+    for (int i = tid; i < Q * LW; i += 512) Ws[i] = E(0);
     put_bc(mem.HC, Cp, a.C_t);
     __syncthreads();
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
-        const int r = own_r<TT>(wv, o), q = own_q<TT>(wv, o);
-        if (r < 0) continue;
+        const int idx = wv + 8 * o, q = tile_q(idx), r = tile_r(idx);
+        if (idx >= TRI) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             IO::store(Ws, (16 * q + 4 * g + i) * LW + M::pos(16 * r + l), W[o][i]);
     }
     __syncthreads();
+    if (q0 >= TT) return;
 #pragma unroll
     for (int n = 0; n < NW; ++n) {
-        const int nt = wv * NW + n;
-        if (nt >= NT) break;
 #pragma unroll
         for (int m = 0; m < KS; ++m) {
-            const Frag bf = M::template col_perm<FOUR>(mem.B + 32 * m * LB + M::pos(16 * nt), LB, g, l);
-            const Frag cf = M::template col_perm<FOUR>(mem.HC + 32 * m * LB + M::pos(16 * nt), LB, g, l);
+            const int at = 32 * m * LB + M::pos(16 * (nt0 + n));
+            const Frag bf = M::template col_perm<FOUR>(mem.B + at, LB, g, l);
+            const Frag cf = M::template col_perm<FOUR>(mem.HC + at, LB, g, l);
 #pragma unroll
-            for (int q = 0; q < TT; ++q) {
-                dC[q][n] = M::mma(M::row_perm(Ws + (16 * q + l) * LW + 32 * m, g), bf, dC[q][n]);
-                dB[q][n] = M::mma(M::template col_perm<FOUR>(Ws + 32 * m * LW + M::pos(16 * q), LW, g, l), cf,
-                                  dB[q][n]);
+            for (int q = 0; q < QR; ++q) {
+                dC[q][n] = M::mma(M::row_perm(Ws + (16 * (q0 + q) + l) * LW + 32 * m, g), bf, dC[q][n]);
+                dB[q][n] = M::mma(M::template col_perm<FOUR>(Ws + 32 * m * LW + M::pos(16 * (q0 + q)), LW, g, l),
+                                  cf, dB[q][n]);
             }
         }
-        const int col = 16 * nt + l;
+        const int col = 16 * (nt0 + n) + l;
         if (col >= N) continue;
 #pragma unroll
-        for (int q = 0; q < TT; ++q)
+        for (int q = 0; q < QR; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = 16 * q + 4 * g + i;
+                const int t = 16 * (q0 + q) + 4 * g + i;
                 if (t >= k.n) continue;
                 const int64_t o = ((k.b * a.L + k.t + t) * G + gr) * N + col;
                 if (a.hsplit > 1) {
@@ -995,7 +994,11 @@ __global__ __launch_bounds__(256) void heads_grad_kernel(HeadsArgs a, const Grad
     const double before = __shfl_up(cols, 1, 16);
     const double pd = static_cast<double>(p) * dt;
     const double rs = lane_prefix(static_cast<double>(r)), ps = lane_prefix(pd);
-    const double X = direct ? static_cast<double>(dec) * ((rc.xdot[0] + rc.xdot[1]) + (rc.xdot[2] + rc.xdot[3]))
+    float xdot = 0.0f;
+    if (direct)
+#pragma unroll
+        for (int w = 0; w < 8; ++w) xdot += rc.xdot[w];
+    const double X = direct ? static_cast<double>(dec) * xdot
                             : a.through[ci * a.H + h];
     const double grad = X + (lane_value(rs, 63) - rs + r) + (ps - pd) + whole + rows + (l ? before : 0.0);
     const float ddt = cv + p + a.A[h] * static_cast<float>(grad);
@@ -1091,7 +1094,7 @@ static hipError_t bwd_go(const HeadsArgs &a, hipStream_t s) {
                            s, a);
     }
     hipLaunchKernelGGL((heads_chunk_bwd_kernel<IO, NP, Q, PS, WIDE>),
-                       dim3(static_cast<unsigned>(chunks * a.G * a.hsplit)), dim3(256), lds, s, a, rec);
+                       dim3(static_cast<unsigned>(chunks * a.G * a.hsplit)), dim3(512), lds, s, a, rec);
     hipLaunchKernelGGL((heads_grad_kernel<IO, Q>), dim3(static_cast<unsigned>((chunks * a.H + 3) / 4)),
                        dim3(256), 0, s, a, rec);
     return hipGetLastError();

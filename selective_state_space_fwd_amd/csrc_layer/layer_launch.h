@@ -64,7 +64,7 @@ hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s);
 // Chunks between two float32 copies of the states in the backward.
 constexpr int kAnchor = 2;
 // Bytes that a chunk's products leave for the gradient of its decays.
-constexpr int kGradRec = 1808;
+constexpr int kGradRec = 1824;
 
 // One chunk of the scan over heads: tokens t .. t + n - 1 of sequence `row`.
 struct HeadsEntry {
