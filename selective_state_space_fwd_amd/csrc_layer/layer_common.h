@@ -6,6 +6,15 @@
 
 namespace ssm {
 
+// Two values to bfloat16 in one instruction, nearest even.  (The header's
+// conversion of two becomes two instructions, a shift and an or: 348 against
+// 310 us of the backward walks at 4 x 2048 x 80 heads.)
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+}
+
 // VW consecutive values of a row as they lie in memory (one access of up to
 // 16 bytes), and as floats.
 template <class IO, int VW>
@@ -42,7 +51,7 @@ __device__ __forceinline__ void store_vec(typename IO::T *p, const float (&o)[VW
     } else if constexpr (sizeof(typename IO::T) == 2) {
         uint32_t raw[VW / 2];
 #pragma unroll
-        for (int i = 0; i < VW; i += 2) raw[i / 2] = Seg<BF16>::pk(o[i], o[i + 1]);
+        for (int i = 0; i < VW; i += 2) raw[i / 2] = pack2(o[i], o[i + 1]);
         __builtin_memcpy(__builtin_assume_aligned(p, VW * 2), raw, VW * 2);
     } else {
 #pragma unroll

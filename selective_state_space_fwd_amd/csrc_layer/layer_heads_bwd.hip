@@ -272,11 +272,11 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
         __syncthreads();
         if (FULL && k.n > 0) {
             // ---- leave the state: a lane's values side by side
-            if (!idle) {
-                const Rsrc to = view(static_cast<E *>(dir ? a.gout : a.hin) + (c * slices + slice) * NT * 256,
-                                     NT * 256 * ES);
+            const Rsrc to = view(static_cast<E *>(dir ? a.gout : a.hin) + (c * slices + slice) * NT * 256,
+                                 idle ? 0 : NT * 256 * ES);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) M::store(M::half(S[nt]), to, lane * 4 * ES, nt * 256 * ES);
+            for (int nt = 0; nt < NT; ++nt) M::store(M::half(S[nt]), to, lane * 4 * ES, nt * 256 * ES);
+            if (!idle) {
                 if (sizeof(E) == 2 && k.first) {
                     // X of a first chunk needs the product with the start state
                     if (dir == 1 && a.h0) {
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
                 }
                 if (sizeof(E) == 2 && dir == 0 && p0 == 0 && lane == 0) a.through[c * H + h] = dec;
             }
-            // ---- and dot it with the other side's tokens
+            // ---- and dot it with the other side's tokens: channels by tokens
             f4 Y[TT];
 #pragma unroll
             for (int q = 0; q < TT; ++q) Y[q] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -317,32 +317,21 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
 #pragma unroll
                 for (int z = 0; z < M::kTerms; ++z)
 #pragma unroll
-                    for (int q = 0; q < TT; ++q) Y[q] = M::mma(rf[q], hf[z], Y[q]);
+                    for (int q = 0; q < TT; ++q) Y[q] = M::mma(hf[z], rf[q], Y[q]);
             }
-            float total = 0.0f;
-            const Rsrc rp = view(a.rp + ((dir * chunks + c) * slices + slice) * Q, idle ? 0 : Q * 4);
-            const uint32_t ro_ = l == 0 ? g * 16 : kDrop;
+            float sum[TT];
 #pragma unroll
-            for (int m = 0; m < KS; ++m) {
-                float y[8];     // the operand's values are where the result's are
-                M::unpack(M::col_perm(mem.Y + 32 * m * LU + 16 * wv, LU, g, l), y);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int q = 2 * m + e;
-                    f4 d;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[i] = row_sum(Y[q][i] * y[4 * e + i]);
-                    // kept without the decay (and dt) to the chunk's end
-                    store16(d, rp, ro_, 64 * q);
-                    if (sizeof(E) == 4) continue;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[i] *= __shfl(ts, 16 * q + 4 * g + i, 64);
-                    total += (d.x + d.y) + (d.z + d.w);
-                }
+            for (int q = 0; q < TT; ++q) {
+                const f4 y = M::fours(mem.Y + (16 * q + l) * LU + 16 * wv + 4 * g);
+                sum[q] = __builtin_fmaf(Y[q].x, y.x, Y[q].y * y.y) + __builtin_fmaf(Y[q].z, y.z, Y[q].w * y.w);
             }
+            // a lane its token's; kept without the decay (and dt) to the chunk's end
+            const float own = group_sums<TT>(sum);
+            if (lane < Q && !idle) a.rp[((dir * chunks + c) * slices + slice) * Q + lane] = own;
             if constexpr (sizeof(E) == 2) {
-                total += __shfl_xor(total, 16, 64);
-                total += __shfl_xor(total, 32, 64);
+                float total = row_sum(lane < Q ? own * ts : 0.0f);
+                total = swap16_add(total, total);
+                total = swap32_add(total, total);
                 if (lane == 0 && !idle) a.rpsum[(dir * chunks + c) * slices + slice] = total;
             }
         }
@@ -1052,7 +1041,7 @@ __global__ __launch_bounds__(256) void heads_blocks_kernel(HeadsArgs a) {
             for (int64_t x = 0; x < a.hsplit; ++x) v += *reinterpret_cast<const f4 *>(p + x * n + i);
             if constexpr (sizeof(E) == 2)
                 *reinterpret_cast<uint2 *>(out + i) =
-                    make_uint2(Seg<BF16>::pk(v.x, v.y), Seg<BF16>::pk(v.z, v.w));
+                    make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
             else
 #pragma unroll
                 for (int e = 0; e < 4; ++e) out[i + e] = v[e];

@@ -84,9 +84,14 @@ struct Mat<BF16> {
         b.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L3 *)(p + 16 * stride));
         return b.f;
     }
+    static __device__ __forceinline__ f4 fours(const E *p) {
+        const uint2 d = *reinterpret_cast<const uint2 *>(p);
+        return f4{__uint_as_float(d.x << 16), __uint_as_float(d.x & 0xffff0000u),
+                  __uint_as_float(d.y << 16), __uint_as_float(d.y & 0xffff0000u)};
+    }
     static __device__ __forceinline__ Frag pack(const float (&v)[8]) {
         Bits b;
-        b.q = Seg<BF16>::pack(v);
+        b.q = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
         return b.f;
     }
     static __device__ __forceinline__ void unpack(Frag f, float (&v)[8]) {
@@ -97,7 +102,7 @@ struct Mat<BF16> {
     // half an operand (one result tile) in LDS: 8 bytes a lane
     using Half = uint2;
     static __device__ __forceinline__ Half half(f4 v) {
-        return make_uint2(Seg<BF16>::pk(v.x, v.y), Seg<BF16>::pk(v.z, v.w));
+        return make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
     }
     static __device__ __forceinline__ void store(Half h, Rsrc to, uint32_t off, int more) {
         typedef uint32_t u2 __attribute__((ext_vector_type(2)));
@@ -154,6 +159,7 @@ struct Mat<F32> {
         for (int j = 0; j < 8; ++j) f[j] = m[(4 * g + (j & 3) + 16 * (j >> 2)) * stride + l];
         return f;
     }
+    static __device__ __forceinline__ f4 fours(const E *p) { return *reinterpret_cast<const f4 *>(p); }
     static __device__ __forceinline__ Frag pack(const float (&v)[8]) {
         return Frag{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
     }
@@ -257,6 +263,25 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
     const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
     const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
     return __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// a + b over the groups of 16 lanes, two values at once: lane group 0 and 2 of
+// a where 16, the lower half of a where 32 lanes change places with b's.
+__device__ __forceinline__ float swap16_add(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float swap32_add(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// Sums over the four groups of lanes: v[q] of tile q -> lane (g, l) has tile
+// g's (of two tiles g % 2's), column l.
+template <int TT>
+__device__ __forceinline__ float group_sums(const float (&v)[TT]) {
+    const float a = swap16_add(v[0], v[1]);
+    if constexpr (TT == 2) return swap32_add(a, a);
+    else return swap32_add(a, swap16_add(v[2], v[3]));
 }
 
 // 2^x of an exponent in 64 bits: what its rounding to float leaves out comes
