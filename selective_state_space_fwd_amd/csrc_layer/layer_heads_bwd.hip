@@ -23,6 +23,8 @@
 // dA in float32 and so are taken from the float32 state there.  Then every
 // chunk is on its own: a workgroup takes a chunk of a group, loops over its
 // heads, and sums dB and dC over them in registers, in a fixed order.
+#include <type_traits>
+
 #include "layer_mat.h"
 
 namespace ssm {
@@ -93,7 +95,11 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
     const float bias = a.bias ? a.bias[h] : 0.0f;
     float *ws = mem.tok[wv];
     const int64_t slices = a.H * sph, slice = static_cast<int64_t>(h) * sph + p0 / 16;
-    const int64_t chunks = a.batch * a.nc, row0 = b * a.nc;
+    // of the wavefront, in the walk's first chunk (of the row)
+    const int64_t slot0 = (dir * a.batch + b) * a.nc * slices + slice;
+    E *left = static_cast<E *>(dir ? a.gout : a.hin) + (b * a.nc * slices + slice) * NT * 256;
+    float *rp0 = a.rp + slot0 * Q, *rpsum0 = a.rpsum + slot0;
+    float *anchor0 = a.anchor + ((dir * a.batch + b) * a.na * slices + slice) * NT * 256;
 
     f4 S[NT];
     auto state_at = [&](int N_, int nt, int i) -> uint32_t {
@@ -147,8 +153,10 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
     double ldec = 0.0;
     bool restarts = false;
 
-    const int64_t xt = dir ? a.dy_t : a.u_t, yt = dir ? a.u_t : a.dy_t;
-    const int64_t kt = dir ? a.C_t : a.B_t, rt = dir ? a.B_t : a.C_t;
+    // WIDE: the strides are small enough for 32 bits
+    using Stride = typename std::conditional<WIDE, int, int64_t>::type;
+    const Stride xt = static_cast<Stride>(dir ? a.dy_t : a.u_t), yt = static_cast<Stride>(dir ? a.u_t : a.dy_t);
+    const Stride kt = static_cast<Stride>(dir ? a.C_t : a.B_t), rt = static_cast<Stride>(dir ? a.B_t : a.C_t);
     const E *Xp = static_cast<const E *>(dir ? a.dy : a.u) + b * (dir ? a.dy_b : a.u_b) + gr * hpg * P;
     const E *Yp = static_cast<const E *>(dir ? a.u : a.dy) + b * (dir ? a.u_b : a.dy_b) + gr * hpg * P;
     const E *Kp = static_cast<const E *>(dir ? a.C : a.B) + b * (dir ? a.C_b : a.B_b) + gr * N;
@@ -231,10 +239,11 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
         // addresses are made here, not kept (and spilled) over the walk
         asm volatile("" : "+v"(l), "+v"(g), "+v"(lane), "+v"(tid));
         const Chunk k = next;
-        const int64_t c = row0 + (dir ? c0 + c1 - 1 - x : x);
+        const int c = dir ? c0 + c1 - 1 - x : x;            // of the row
         if (x + 1 < c1) next = chunk(x + 1); else next.n = 0;
         if (k.n > 0 && (dir ? k.last : k.first)) {
-            const float *from = dir ? a.dlast : a.h0;
+            const ArgsAgain q = args_again();
+            const float *from = dir ? q->dlast : q->h0;
             if (from) load_state(S, from, k.row); else clear_state();
             restarts = true;
         }
@@ -272,16 +281,16 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
         __syncthreads();
         if (FULL && k.n > 0) {
             // ---- leave the state: a lane's values side by side
-            const Rsrc to = view(static_cast<E *>(dir ? a.gout : a.hin) + (c * slices + slice) * NT * 256,
-                                 idle ? 0 : NT * 256 * ES);
+            const Rsrc to = view(left + c * slices * (NT * 256), idle ? 0 : NT * 256 * ES);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) M::store(M::half(S[nt]), to, lane * 4 * ES, nt * 256 * ES);
             if (!idle) {
                 if (sizeof(E) == 2 && k.first) {
                     // X of a first chunk needs the product with the start state
-                    if (dir == 1 && a.h0) {
+                    const ArgsAgain again = args_again();
+                    if (dir == 1 && again->h0) {
                         f4 h0[NT];
-                        load_state(h0, a.h0, k.row);
+                        load_state(h0, again->h0, k.row);
                         float v = 0.0f;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -290,16 +299,15 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
                         }
 #pragma unroll
                         for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-                        if (lane == 0) a.hdot[k.row * slices + slice] = v;
+                        if (lane == 0) again->hdot[k.row * slices + slice] = v;
                     }
-                } else if (sizeof(E) == 2 && (c - row0) % kAnchor == 0 && dec >= kDirect) {
-                    const Rsrc an = view(
-                        a.anchor + (((dir * a.batch + b) * a.na + (c - row0) / kAnchor) * slices + slice) * NT * 256,
-                        NT * 256 * 4);
+                } else if (sizeof(E) == 2 && c % kAnchor == 0 && dec >= kDirect) {
+                    const Rsrc an = view(anchor0 + c / kAnchor * slices * (NT * 256), NT * 256 * 4);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) store16(S[nt], an, lane * 16, nt * 1024);
                 }
-                if (sizeof(E) == 2 && dir == 0 && p0 == 0 && lane == 0) a.through[c * H + h] = dec;
+                if (sizeof(E) == 2 && dir == 0 && p0 == 0 && lane == 0)
+                    a.through[(static_cast<int64_t>(b) * a.nc + c) * H + h] = dec;
             }
             // ---- and dot it with the other side's tokens: channels by tokens
             f4 Y[TT];
@@ -327,12 +335,12 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
             }
             // a lane its token's; kept without the decay (and dt) to the chunk's end
             const float own = group_sums<TT>(sum);
-            if (lane < Q && !idle) a.rp[((dir * chunks + c) * slices + slice) * Q + lane] = own;
+            if (lane < Q && !idle) rp0[c * slices * Q + lane] = own;
             if constexpr (sizeof(E) == 2) {
                 float total = row_sum(lane < Q ? own * ts : 0.0f);
                 total = swap16_add(total, total);
                 total = swap32_add(total, total);
-                if (lane == 0 && !idle) a.rpsum[(dir * chunks + c) * slices + slice] = total;
+                if (lane == 0 && !idle) rpsum0[c * slices] = total;
             }
         }
         if constexpr (FULL && WIDE) {
@@ -368,7 +376,10 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (FULL && dir == 1 && k.n > 0 && k.first && a.dh0) store_state(a.dh0, k.row);
+        if (FULL && dir == 1 && k.n > 0 && k.first) {
+            float *dh0 = args_again()->dh0;
+            if (dh0) store_state(dh0, k.row);
+        }
         __syncthreads();
     }
     if constexpr (!FULL) {
@@ -527,7 +538,6 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     const int slices = H * sph;
 
     const E *Bp = static_cast<const E *>(a.B) + k.b * a.B_b + k.t * a.B_t + gr * N;
-    const E *Cp = static_cast<const E *>(a.C) + k.b * a.C_b + k.t * a.C_t + gr * N;
     const E *Up = static_cast<const E *>(a.u) + k.b * a.u_b + k.t * a.u_t;
     const E *Yp = static_cast<const E *>(a.dy) + k.b * a.dy_b + k.t * a.dy_t;
     const E *Tp = static_cast<const E *>(a.delta) + k.b * a.dt_b + k.t * a.dt_t;
@@ -601,7 +611,7 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     };
 
     put_bc(mem.B, Bp, a.B_t);
-    put_bc(mem.HC, Cp, a.C_t);
+    put_bc(mem.HC, static_cast<const E *>(a.C) + k.b * a.C_b + k.t * a.C_t + gr * N, a.C_t);
     __syncthreads();
     f4 CB[OWN], W[OWN], DX[OWN], dB[QR][NW], dC[QR][NW];
     const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -868,9 +878,10 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         p0 = pn;
     }
     // ---- W over all heads, rows t by columns s, nothing above the diagonal
+    const ArgsAgain z = args_again();
     E *Ws = mem.G;
     for (int i = tid; i < Q * LW; i += 512) Ws[i] = E(0);
-    put_bc(mem.HC, Cp, a.C_t);
+    put_bc(mem.HC, static_cast<const E *>(z->C) + k.b * z->C_b + k.t * z->C_t + gr * N, z->C_t);
     __syncthreads();
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
@@ -904,14 +915,14 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
             for (int i = 0; i < 4; ++i) {
                 const int t = 16 * (q0 + q) + 4 * g + i;
                 if (t >= k.n) continue;
-                const int64_t o = ((k.b * a.L + k.t + t) * G + gr) * N + col;
-                if (a.hsplit > 1) {
-                    const int64_t all = a.batch * a.L * G * N;
-                    a.dBp[hs * all + o] = dB[q][n][i];
-                    a.dCp[hs * all + o] = dC[q][n][i];
+                const int64_t o = ((k.b * z->L + k.t + t) * G + gr) * N + col;
+                if (z->hsplit > 1) {
+                    const int64_t all = z->batch * z->L * G * N;
+                    z->dBp[hs * all + o] = dB[q][n][i];
+                    z->dCp[hs * all + o] = dC[q][n][i];
                 } else {
-                    IO::store(static_cast<E *>(a.dB), o, dB[q][n][i]);
-                    IO::store(static_cast<E *>(a.dC), o, dC[q][n][i]);
+                    IO::store(static_cast<E *>(z->dB), o, dB[q][n][i]);
+                    IO::store(static_cast<E *>(z->dC), o, dC[q][n][i]);
                 }
             }
     }

@@ -28,6 +28,16 @@ __device__ __forceinline__ void store16(f4 v, Rsrc to, uint32_t off, int more) {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), to, off, more, 0);
 }
 
+// The kernel's arguments read again: what a loop needs rarely, or only the end
+// does, takes no scalar registers (or lanes of a vector one) until then.  The
+// arguments are the kernel's first.
+typedef const __attribute__((address_space(4))) HeadsArgs *ArgsAgain;
+__device__ __forceinline__ ArgsAgain args_again() {
+    ArgsAgain p = (ArgsAgain)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
 // A number known while compiling, for lambdas.
 template <int I>
 struct Int { static constexpr int value = I; };
