@@ -478,7 +478,8 @@ struct ChunkMem {
     static constexpr int kC = (Q > PS ? Q : PS) * LB;
     __attribute__((aligned(16))) E B[Q * LB];
     __attribute__((aligned(16))) E HC[kC];                      // h_in; C
-    __attribute__((aligned(16))) E G[PS * LB > Q * LW ? PS * LB : Q * LW];     // gh; at last W
+    static constexpr int WT = sizeof(E) == 2 ? 2 : 1;           // values that hold one of W
+    __attribute__((aligned(16))) E G[PS * LB > WT * Q * LW ? PS * LB : WT * Q * LW];   // gh; at last W
     __attribute__((aligned(16))) E U[Q * LU];
     __attribute__((aligned(16))) E Y[Q * LU];
     __attribute__((aligned(16))) typename M::Half Mh[TRI * 64];
@@ -880,7 +881,7 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
     // ---- W over all heads, rows t by columns s, nothing above the diagonal
     const ArgsAgain z = args_again();
     E *Ws = mem.G;
-    for (int i = tid; i < Q * LW; i += 512) Ws[i] = E(0);
+    for (int i = tid; i < Mem::WT * Q * LW; i += 512) Ws[i] = E(0);
     put_bc(mem.HC, static_cast<const E *>(z->C) + k.b * z->C_b + k.t * z->C_t + gr * N, z->C_t);
     __syncthreads();
 #pragma unroll
@@ -888,8 +889,13 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
         const int idx = wv + 8 * o, q = tile_q(idx), r = tile_r(idx);
         if (idx >= TRI) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            IO::store(Ws, (16 * q + 4 * g + i) * LW + M::pos(16 * r + l), W[o][i]);
+        for (int i = 0; i < 4; ++i) {
+            // in two values of 16 bits: a sum over all heads, rounded to one it
+            // would add as much again to the error of dB and dC
+            const int at = (16 * q + 4 * g + i) * LW + M::pos(16 * r + l);
+            IO::store(Ws, at, W[o][i]);
+            if constexpr (Mem::WT == 2) IO::store(Ws, Q * LW + at, W[o][i] - IO::load(Ws, at));
+        }
     }
     __syncthreads();
     if (q0 >= TT) return;
@@ -901,11 +907,14 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
             const Frag bf = M::template col_perm<FOUR>(mem.B + at, LB, g, l);
             const Frag cf = M::template col_perm<FOUR>(mem.HC + at, LB, g, l);
 #pragma unroll
-            for (int q = 0; q < QR; ++q) {
-                dC[q][n] = M::mma(M::row_perm(Ws + (16 * (q0 + q) + l) * LW + 32 * m, g), bf, dC[q][n]);
-                dB[q][n] = M::mma(M::template col_perm<FOUR>(Ws + 32 * m * LW + M::pos(16 * (q0 + q)), LW, g, l),
-                                  cf, dB[q][n]);
-            }
+            for (int q = 0; q < QR; ++q)
+#pragma unroll
+                for (int t = 0; t < Mem::WT; ++t) {
+                    const E *w = Ws + t * Q * LW;
+                    dC[q][n] = M::mma(M::row_perm(w + (16 * (q0 + q) + l) * LW + 32 * m, g), bf, dC[q][n]);
+                    dB[q][n] = M::mma(M::template col_perm<FOUR>(w + 32 * m * LW + M::pos(16 * (q0 + q)), LW, g, l),
+                                      cf, dB[q][n]);
+                }
         }
         const int col = 16 * (nt0 + n) + l;
         if (col >= N) continue;
