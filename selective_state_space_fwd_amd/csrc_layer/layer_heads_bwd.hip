@@ -83,10 +83,11 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
     const int N = static_cast<int>(a.N), P = static_cast<int>(a.P), H = static_cast<int>(a.H);
     const int hpg = static_cast<int>(a.H / a.G), sph = (P + 15) / 16, per = (hpg * sph + 3) / 4;
     const int wgs = static_cast<int>(a.G) * per, J = static_cast<int>(a.J);
-    const int half = wgs * J * static_cast<int>(a.batch);
+    const int ranges = FULL ? J : J - 1;    // nobody needs the end of a walk's last
+    const int half = wgs * ranges * static_cast<int>(a.batch);
     const int all = static_cast<int>(by_xcd(blockIdx.x, gridDim.x));
     const int dir = all >= half, id = all - (dir ? half : 0);
-    const int wg = id % wgs, j = id / wgs % J, b = id / (wgs * J);
+    const int wg = id % wgs, j = id / wgs % ranges + (!FULL && dir), b = id / (wgs * ranges);
     const int gr = wg / per, is0 = wg % per * 4, is = is0 + wv;
     const bool idle = is >= hpg * sph;
     const int h = gr * hpg + (idle ? 0 : is / sph), p0 = idle ? 0 : is % sph * 16;
@@ -1084,17 +1085,19 @@ static hipError_t bwd_go(const HeadsArgs &a, hipStream_t s) {
     static_assert(sizeof(GradRec<Q>) <= kGradRec, "workspace of a chunk and head");
     const int64_t hpg = a.H / a.G, sph = (a.P + 15) / 16;
     const int64_t wgs = a.G * ((hpg * sph + 3) / 4), chunks = a.batch * a.nc;
-    const unsigned walks = static_cast<unsigned>(2 * wgs * a.J * a.batch);
+    const unsigned walks = static_cast<unsigned>(2 * wgs * a.batch);     // of one range
     GradRec<Q> *rec = reinterpret_cast<GradRec<Q> *>(a.rec);
     if (a.J > 1) {
-        hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, false, WIDE>), dim3(walks), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, false, WIDE>),
+                           dim3(walks * static_cast<unsigned>(a.J - 1)), dim3(256), 0, s, a);
         hipError_t e = launch_heads_join(a, a.hend, a.ldec, 0, s);
         if (e == hipSuccess)
             e = launch_heads_join(a, a.hend + a.batch * a.J * a.H * a.P * a.N,
                                   a.ldec + a.batch * a.J * a.H, 1, s);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, true, WIDE>), dim3(walks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, true, WIDE>),
+                       dim3(walks * static_cast<unsigned>(a.J)), dim3(256), 0, s, a);
     if constexpr (sizeof(E) == 2) {
         hipLaunchKernelGGL(heads_anchor_kernel, dim3(static_cast<unsigned>(a.batch * a.na * a.H)),
                            dim3(256), 0, s, a, NP);
@@ -1132,14 +1135,9 @@ static hipError_t bwd_io(const HeadsArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_heads_bwd(const HeadsArgs &a, hipStream_t s) {
-    hipError_t e = hipSuccess;
-    if (a.dh0 && a.rows > 0 && (a.cu || a.L == 0)) e = launch_heads_empty(a, a.dlast, a.dh0, s);
+    hipError_t e = launch_heads_rows(a, a.dlast, a.dh0, s);
     if (e != hipSuccess) return e;
     if (a.L > 0 && a.batch > 0) {
-        if (a.cu) {
-            e = launch_heads_table(a, const_cast<HeadsEntry *>(a.table), s);
-            if (e != hipSuccess) return e;
-        }
         e = a.bf16 ? bwd_io<BF16>(a, s) : bwd_io<F32>(a, s);
         if (e != hipSuccess) return e;
     }

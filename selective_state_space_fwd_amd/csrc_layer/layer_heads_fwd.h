@@ -103,7 +103,8 @@ __global__ __launch_bounds__(256, (fwd_waves<IO, NP, HW, Q, FULL>())) void heads
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     int lane = tid & 63, g = lane >> 4, l = lane & 15;
     const int id = static_cast<int>(by_xcd(blockIdx.x, gridDim.x));
-    const int wg = id % a.wgs, j = id / a.wgs % a.J, b = id / (a.wgs * a.J);
+    const int ranges = FULL ? a.J : a.J - 1;    // nobody needs the end of the last
+    const int wg = id % a.wgs, j = id / a.wgs % ranges, b = id / (a.wgs * ranges);
     const int gr = wg / a.per, in = wg % a.per;
     // the slice of channels of column block w: its head (of this workgroup's,
     // hs) and first channel; a head past the group's: none
@@ -481,13 +482,15 @@ template <class IO, int NP, int HW, int Q, bool WIDE>
 hipError_t heads_fwd_go(const HeadsArgs &a, FwdK k, hipStream_t s) {
     k.per = heads_wgs<HW>(a);
     k.wgs = static_cast<int>(a.G * k.per);
-    const unsigned grid = static_cast<unsigned>(k.wgs * a.J * a.batch);
+    const unsigned grid = static_cast<unsigned>(k.wgs * a.batch);     // of one range
     if (a.J > 1) {
-        hipLaunchKernelGGL((heads_fwd_kernel<IO, NP, HW, Q, false, WIDE>), dim3(grid), dim3(256), 0, s, k);
+        hipLaunchKernelGGL((heads_fwd_kernel<IO, NP, HW, Q, false, WIDE>),
+                           dim3(grid * static_cast<unsigned>(a.J - 1)), dim3(256), 0, s, k);
         const hipError_t e = launch_heads_join(a, a.hend, a.ldec, 0, s);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((heads_fwd_kernel<IO, NP, HW, Q, true, WIDE>), dim3(grid), dim3(256), 0, s, k);
+    hipLaunchKernelGGL((heads_fwd_kernel<IO, NP, HW, Q, true, WIDE>),
+                       dim3(grid * static_cast<unsigned>(a.J)), dim3(256), 0, s, k);
     return hipGetLastError();
 }
 
