@@ -53,10 +53,12 @@ struct HeadsPlan {
            anchor = 0, adot = 0, rec = 0, part = 0, dBp = 0, dCp = 0, bytes = 0;
 };
 
-// A walk is serial over its chunks, and a compute unit holds about two of its
-// workgroups.  Below one workgroup a compute unit the rows are cut into
-// ranges of at least 4 chunks, for about two a compute unit: the launch that
-// finds the ranges' states costs about half a walk more.
+// A walk is serial over its chunks, and a compute unit holds three of its
+// workgroups (at 128 states).  Below one workgroup a compute unit the rows are
+// cut into ranges of at least 4 chunks, for about three a compute unit; the
+// launch that finds the ranges' states costs half a walk more.  (1 x 65536 x 32
+// heads: pre-pass, join and walk 503 us aimed at 768 workgroups, 553 at 512,
+// 562 at 1024.)
 ssm_status plan_heads(const ssm_heads_desc *d, bool bwd, HeadsPlan *p) {
     const int bf16 = d->io_dtype == SSM_BF16;
     const int64_t hpg = d->heads / d->groups;
@@ -70,6 +72,8 @@ ssm_status plan_heads(const ssm_heads_desc *d, bool bwd, HeadsPlan *p) {
     p->sph = ceil_div(d->head_dim, 16);
     p->wgs = d->groups * ceil_div(hpg * p->sph, 4);
     const int64_t base = d->batch * p->wgs * (bwd ? 2 : 1);
+    // the most that a walk of one head a workgroup takes, should it be more
+    const int64_t most = d->batch * d->heads * ceil_div(p->sph, 4) * (bwd ? 2 : 1);
     p->Kc = p->nc > 0 ? p->nc : 1;
     if (base > 0 && base < 256 && p->nc >= 8) {
         int64_t J = ceil_div(768, base);
@@ -78,7 +82,7 @@ ssm_status plan_heads(const ssm_heads_desc *d, bool bwd, HeadsPlan *p) {
     }
     p->J = p->nc > 0 ? ceil_div(p->nc, p->Kc) : 1;
     const int64_t chunks = d->batch * p->nc;
-    if (static_cast<double>(base) * p->J > kMaxGrid) return SSM_ERR_UNSUPPORTED;
+    if (static_cast<double>(base > most ? base : most) * p->J > kMaxGrid) return SSM_ERR_UNSUPPORTED;
     size_t at = 0;
     auto take = [&](double n, double esz) {
         const size_t o = at;
@@ -93,9 +97,13 @@ ssm_status plan_heads(const ssm_heads_desc *d, bool bwd, HeadsPlan *p) {
     }
     if (bwd) {
         if (d->batch > 65535) return SSM_ERR_UNSUPPORTED;
-        // blocks of a group's heads: about four workgroups a compute unit
+        // Blocks of a group's heads, each a workgroup a chunk, for two workgroups
+        // a compute unit, which is what one holds; the blocks' dB and dC are then
+        // added.  More blocks add more, fewer leave units empty: 1 x 2048, 2 x
+        // 2048 and 4 x 2048 x 80 heads 224, 326 and 566 us; aimed at 1024
+        // workgroups 250, 346 and 579, at 256 224, 351 and 623.
         p->hsplit = 1;
-        if (chunks > 0 && chunks * d->groups < 1024) p->hsplit = ceil_div(1024, chunks * d->groups);
+        if (chunks > 0 && chunks * d->groups < 512) p->hsplit = ceil_div(512, chunks * d->groups);
         if (p->hsplit > hpg) p->hsplit = hpg;
         p->hblk = ceil_div(hpg, p->hsplit);
         p->hsplit = ceil_div(hpg, p->hblk);

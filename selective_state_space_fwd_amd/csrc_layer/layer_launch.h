@@ -61,7 +61,9 @@ int64_t norm_bwd_blocks(int64_t rows, int64_t d, int64_t group);
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s);
 
-// Chunks between two float32 copies of the states in the backward.
+// Chunks between two float32 copies of the states in the backward (bfloat16).
+// At 4 x 2048 x 80 heads dA is off by 3e-7 of its norm with 2; with 4 by 1.4e-6
+// for 50 us of 570 less, and a sharper head's up to 3e-6 with 8.
 constexpr int kAnchor = 2;
 // Bytes that a chunk's products leave for the gradient of its decays.
 constexpr int kGradRec = 1824;

@@ -2,14 +2,12 @@
 //
 // Operand layout of a product with 32 values of k (a wavefront of 4 groups g
 // of 16 lanes l): lane (g, l) holds 8 values of k of row (or column) l.  Which
-// 8 does not matter as long as both operands agree, and three orders occur:
-//   row       k = 8g .. 8g+7                     (16 neighbouring bytes)
-//   row_perm  k = 4g .. 4g+3, 16+4g .. 16+4g+3
-//   col_perm  the same k, read down a column of a matrix stored by rows of k
-// 16-bit rows that are read in the permuted order are kept so in LDS (pos):
-// one read of 16 bytes instead of two of 8, which run at half the rate at
-// every distance of the rows (measured: 31 .. 37 against 66 cycles for the four
-// wavefronts' 4 KB).
+// 8 does not matter as long as both operands agree; here k = 4g .. 4g+3 and
+// 16+4g .. 16+4g+3 (the permuted order), read along a row (row_perm) or down a
+// column of a matrix stored by rows of k (col_perm).  16-bit rows are kept in
+// the permuted order in LDS (pos): one read of 16 bytes instead of two of 8,
+// which run at half the rate at every distance of the rows (measured: 31 .. 37
+// against 66 cycles for the four wavefronts' 4 KB).
 // A result tile has rows 4g .. 4g+3 of column l in lane (g, l): two result
 // tiles one above the other are an operand in the permuted order, with no
 // data moved between lanes.
@@ -55,17 +53,16 @@ struct Mat<BF16> {
     static __device__ __forceinline__ f4 mma(Frag a, Frag b, f4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
-    static __device__ __forceinline__ Frag row(const E *p, int g) {
-        Bits b;
-        b.q = *reinterpret_cast<const uint4 *>(p + 8 * g);
-        return b.f;
-    }
     // where column c of a row kept in the permuted order lies; whole tiles of
     // 16 columns: the tile's first value is at pos, the next fours at pos + 8
     static __device__ __forceinline__ constexpr int pos(int c) {
         return (c & ~31) + (c >> 2 & 3) * 8 + (c >> 4 & 1) * 4 + (c & 3);
     }
-    static __device__ __forceinline__ Frag row_perm(const E *p, int g) { return row(p, g); }
+    static __device__ __forceinline__ Frag row_perm(const E *p, int g) {
+        Bits b;
+        b.q = *reinterpret_cast<const uint4 *>(p + 8 * g);
+        return b.f;
+    }
     // columns c .. c + 7 (c a multiple of 8) into a row kept in that order
     template <class Vec>
     static __device__ __forceinline__ void put_perm(E *row, int c, const Vec &v) {
@@ -147,13 +144,11 @@ struct Mat<F32> {
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
         return c;
     }
-    static __device__ __forceinline__ Frag two(const E *p, const E *q) {
-        const f4 a = *reinterpret_cast<const f4 *>(p), b = *reinterpret_cast<const f4 *>(q);
+    static __device__ __forceinline__ constexpr int pos(int c) { return c; }
+    static __device__ __forceinline__ Frag row_perm(const E *p, int g) {
+        const f4 a = *reinterpret_cast<const f4 *>(p + 4 * g), b = *reinterpret_cast<const f4 *>(p + 16 + 4 * g);
         return Frag{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     }
-    static __device__ __forceinline__ Frag row(const E *p, int g) { return two(p + 8 * g, p + 8 * g + 4); }
-    static __device__ __forceinline__ constexpr int pos(int c) { return c; }
-    static __device__ __forceinline__ Frag row_perm(const E *p, int g) { return two(p + 4 * g, p + 16 + 4 * g); }
     template <class Vec>
     static __device__ __forceinline__ void put_perm(E *row, int c, const Vec &v) {
         *reinterpret_cast<Vec *>(row + c) = v;
@@ -214,30 +209,6 @@ __device__ __forceinline__ Chunk chunk_at(const HeadsArgs &a, int64_t b, int64_t
         k.last = c == a.nc - 1;
     }
     return k;
-}
-
-// Rows of a chunk into LDS: dst[t][c] = src[t * stride + c] for t < n, c < cols,
-// zeros up to Q rows and `width` columns.  vec: 16-byte pieces.
-template <class IO, int Q>
-__device__ __forceinline__ void stage_rows(typename IO::T *dst, int ld, const typename IO::T *src,
-                                           int64_t stride, int n, int cols, int width, bool vec) {
-    using T = typename IO::T;
-    constexpr int V = Seg<IO>::VW;
-    using Vec = typename Seg<IO>::V;
-    if (vec) {
-        const int per = width / V;
-        for (int i = threadIdx.x; i < Q * per; i += blockDim.x) {
-            const int t = i / per, c = (i % per) * V;
-            Vec v{};
-            if (t < n && c < cols) v = *reinterpret_cast<const Vec *>(src + t * stride + c);
-            *reinterpret_cast<Vec *>(dst + t * ld + c) = v;
-        }
-    } else {
-        for (int i = threadIdx.x; i < Q * width; i += blockDim.x) {
-            const int t = i / width, c = i % width;
-            dst[t * ld + c] = t < n && c < cols ? src[t * stride + c] : T(0);
-        }
-    }
 }
 
 // Workgroup id -> position: the ids of one XCD (id % 8) become neighbours, so
@@ -308,15 +279,6 @@ __device__ __forceinline__ float softplus_exact(float x) {
     const float e = exp2_d(static_cast<double>(-fabsf(x)) * 1.4426950408889634);
     const float s = 1.0f + e;
     return fmaxf(x, 0.0f) + __builtin_fmaf(log2_hw(s), kLn2, (1.0f - s) + e);
-}
-
-// The step size of one token of one head (0 behind the chunk's end).
-template <class IO>
-__device__ __forceinline__ float step_size(const HeadsArgs &a, const Chunk &k, int t, int64_t h) {
-    if (t >= k.n) return 0.0f;
-    float v = IO::load(static_cast<const typename IO::T *>(a.delta) + k.b * a.dt_b + (k.t + t) * a.dt_t, h);
-    if (a.bias) v += a.bias[h];
-    return a.softplus ? softplus_exact(v) : v;
 }
 
 // Host: whether rows of `src` can be read in 16-byte pieces.
