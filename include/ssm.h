@@ -1,7 +1,8 @@
 /*
  * ssm.h -- C ABI of libssm, the MI355X (gfx950) selective state-space scan.
  *
- * Two operations, both from the Mamba selective-scan pages:
+ * Two operations, both from the Mamba selective-scan pages (and, further
+ * down, the layer operators with conventions of their own):
  *
  *   ssm_scan_fwd      the fused prefill scan.  Per token it forms the step
  *                     size delta_t = softplus(delta + delta_bias) (SSM

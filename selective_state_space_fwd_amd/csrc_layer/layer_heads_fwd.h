@@ -20,8 +20,8 @@
 // workgroups share a compute unit; its vector units and LDS are each busy about
 // half of the time.  1 x 65536 x 32 heads, 24 ranges: pre-pass 156, join 15, walk
 // 260 us.
-// In float32 a product takes eight instructions of a sixteenth of the rate: 8 x
-// 2048 x 80 heads, 963 us.
+// In float32 the products run at a sixteenth of the rate: 8 x 2048 x 80 heads,
+// 963 us.
 #pragma once
 
 #include "layer_mat.h"
