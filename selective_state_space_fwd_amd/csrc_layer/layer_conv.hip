@@ -287,8 +287,10 @@ __global__ __launch_bounds__(512) void conv_reduce_kernel(ConvArgs a) {
     const int x = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + x;
     float v = 0.0f;
-    if (col < cols)
+    if (col < cols) {
+#pragma unroll 8
         for (int64_t r = w; r < a.runs; r += 16) v += a.part[r * cols + col];
+    }
     sum[w][x] = v;
     for (int n = 8; n > 0; n >>= 1) {
         __syncthreads();

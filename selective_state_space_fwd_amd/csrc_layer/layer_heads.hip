@@ -8,12 +8,15 @@ hipError_t heads_fwd_bf16(const HeadsArgs &a, hipStream_t s);
 hipError_t heads_fwd_f32(const HeadsArgs &a, hipStream_t s);
 
 // Joins the ranges: slot j of hend becomes the state that enters range j + 1
-// (reverse: j - 1).  Nothing enters a range from the last one's end.
-__global__ __launch_bounds__(256) void heads_join_kernel(HeadsArgs a, float *hend, const float *ldec,
-                                                         int reverse) {
+// (against time, blockIdx.z 1: j - 1).  Nothing enters a range from the last
+// one's end.
+__global__ __launch_bounds__(256) void heads_join_kernel(HeadsArgs a) {
     const int64_t per = a.P * a.N, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t h = blockIdx.y % a.H, b = blockIdx.y / a.H;
     if (i >= per) return;
+    const bool reverse = blockIdx.z;
+    float *hend = a.hend + (reverse ? a.batch * a.J * a.H * per : 0);
+    const float *ldec = a.ldec + (reverse ? a.batch * a.J * a.H : 0);
     // eight ranges on their way at a time
     float v = 0.0f;
     for (int64_t x0 = 0; x0 < a.J - 1; x0 += 8) {
@@ -87,12 +90,11 @@ __global__ __launch_bounds__(256) void heads_rows_kernel(HeadsArgs a, HeadsEntry
     }
 }
 
-hipError_t launch_heads_join(const HeadsArgs &a, float *hend, const float *ldec, int reverse,
-                             hipStream_t s) {
+hipError_t launch_heads_join(const HeadsArgs &a, int walks, hipStream_t s) {
     hipLaunchKernelGGL(heads_join_kernel,
                        dim3(static_cast<unsigned>((a.P * a.N + 255) / 256),
-                            static_cast<unsigned>(a.H * a.batch)),
-                       dim3(256), 0, s, a, hend, ldec, reverse);
+                            static_cast<unsigned>(a.H * a.batch), static_cast<unsigned>(walks)),
+                       dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

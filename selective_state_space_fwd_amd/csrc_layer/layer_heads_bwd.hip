@@ -1047,26 +1047,29 @@ __global__ __launch_bounds__(256) void heads_grad_kernel(HeadsArgs a, const Grad
     }
 }
 
-// dA, dD and ddelta_bias: the chunks' shares, added in a fixed order.
-__global__ __launch_bounds__(64) void heads_sums_kernel(HeadsArgs a) {
-    const int64_t h = blockIdx.x, chunks = a.batch * a.nc;
-    float *out = blockIdx.y == 0 ? a.dA : blockIdx.y == 1 ? a.dD : a.dbias;
-    if (!out) return;
+// dA, dD and ddelta_bias (which 0, 1, 2): the chunks' shares, added in a fixed
+// order, a wavefront a head.
+__device__ __forceinline__ void sum_chunks(const HeadsArgs &a, int which, int64_t h) {
+    const int64_t chunks = a.batch * a.nc;
+    float *out = which == 0 ? a.dA : which == 1 ? a.dD : a.dbias;
+    if (!out || h >= a.H) return;
     double v = 0.0;
-    for (int64_t c = threadIdx.x; c < chunks; c += 64)
-        v += a.part[(blockIdx.y * chunks + c) * a.H + h];
+    for (int64_t c = threadIdx.x & 63; c < chunks; c += 64) v += a.part[(which * chunks + c) * a.H + h];
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    if (threadIdx.x == 0) out[h] = static_cast<float>(v);
+    if ((threadIdx.x & 63) == 0) out[h] = static_cast<float>(v);
 }
 
-// dB and dC: the blocks of heads, added in order.
+// The sums over chunks (blockIdx.y 0 .. 2), and dB and dC (3, 4): the blocks of
+// heads, added in order.
 template <class IO>
-__global__ __launch_bounds__(256) void heads_blocks_kernel(HeadsArgs a) {
+__global__ __launch_bounds__(256) void heads_sums_kernel(HeadsArgs a) {
     using E = typename IO::T;
     const int64_t n = a.batch * a.L * a.G * a.N;
-    const float *p = blockIdx.y ? a.dCp : a.dBp;
-    E *out = static_cast<E *>(blockIdx.y ? a.dC : a.dB);
+    if (blockIdx.y < 3)
+        return sum_chunks(a, blockIdx.y, static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6));
+    const float *p = blockIdx.y == 4 ? a.dCp : a.dBp;
+    E *out = static_cast<E *>(blockIdx.y == 4 ? a.dC : a.dB);
     int64_t end = n;
     if (a.cu) end = seq_at(a.cu, a.rows, a.L) * a.G * a.N;      // tokens behind the last sequence
     // four at a time (whole: n and end are multiples of N) where N allows it
@@ -1106,10 +1109,7 @@ static hipError_t bwd_go(const HeadsArgs &a, hipStream_t s) {
     if (a.J > 1) {
         hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, false, WIDE>),
                            dim3(walks * static_cast<unsigned>(a.J - 1)), dim3(256), 0, s, a);
-        hipError_t e = launch_heads_join(a, a.hend, a.ldec, 0, s);
-        if (e == hipSuccess)
-            e = launch_heads_join(a, a.hend + a.batch * a.J * a.H * a.P * a.N,
-                                  a.ldec + a.batch * a.J * a.H, 1, s);
+        const hipError_t e = launch_heads_join(a, 2, s);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((heads_walk_kernel<IO, NP, Q, true, WIDE>),
@@ -1142,11 +1142,16 @@ template <class IO>
 static hipError_t bwd_io(const HeadsArgs &a, hipStream_t s) {
     constexpr bool f32 = sizeof(typename IO::T) == 4;
     constexpr int Q = f32 ? 32 : 64;
-    hipError_t e = a.N <= 32 ? bwd_wide<IO, 32, Q, 64>(a, s) : a.N <= 64 ? bwd_wide<IO, 64, Q, 64>(a, s)
-                   : a.N <= 128 ? bwd_wide<IO, 128, Q, 64>(a, s) : bwd_wide<IO, 256, 32, f32 ? 32 : 64>(a, s);
-    if (e != hipSuccess) return e;
-    if (a.hsplit > 1)
-        hipLaunchKernelGGL((heads_blocks_kernel<IO>), dim3(1024, 2), dim3(256), 0, s, a);
+    return a.N <= 32 ? bwd_wide<IO, 32, Q, 64>(a, s) : a.N <= 64 ? bwd_wide<IO, 64, Q, 64>(a, s)
+           : a.N <= 128 ? bwd_wide<IO, 128, Q, 64>(a, s) : bwd_wide<IO, 256, 32, f32 ? 32 : 64>(a, s);
+}
+
+template <class IO>
+static hipError_t sums_io(const HeadsArgs &a, hipStream_t s) {
+    const bool blocks = a.hsplit > 1 && a.L > 0 && a.batch > 0;
+    const unsigned heads = static_cast<unsigned>((a.H + 3) / 4);
+    hipLaunchKernelGGL((heads_sums_kernel<IO>), dim3(blocks && heads < 1024 ? 1024 : heads, blocks ? 5 : 3),
+                       dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1158,8 +1163,7 @@ hipError_t launch_heads_bwd(const HeadsArgs &a, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     // without a token the sums are zero
-    hipLaunchKernelGGL(heads_sums_kernel, dim3(static_cast<unsigned>(a.H), 3), dim3(64), 0, s, a);
-    return hipGetLastError();
+    return a.bf16 ? sums_io<BF16>(a, s) : sums_io<F32>(a, s);
 }
 
 }  // namespace ssm

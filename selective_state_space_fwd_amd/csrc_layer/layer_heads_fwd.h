@@ -496,7 +496,7 @@ hipError_t heads_fwd_go(const HeadsArgs &a, FwdK k, hipStream_t s) {
     if (a.J > 1) {
         hipLaunchKernelGGL((heads_fwd_kernel<IO, NP, HW, Q, false, WIDE>),
                            dim3(grid * static_cast<unsigned>(a.J - 1)), dim3(256), 0, s, k);
-        const hipError_t e = launch_heads_join(a, a.hend, a.ldec, 0, s);
+        const hipError_t e = launch_heads_join(a, 1, s);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((heads_fwd_kernel<IO, NP, HW, Q, true, WIDE>),

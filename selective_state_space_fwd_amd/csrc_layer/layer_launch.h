@@ -119,7 +119,7 @@ struct HeadsArgs {
 constexpr int heads_np(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 constexpr int heads_fwd_chunk(int bf16, int64_t N) { return !bf16 && N > 128 ? 32 : 64; }
 constexpr int heads_bwd_chunk(int bf16, int64_t N) { return !bf16 || N > 128 ? 32 : 64; }
-hipError_t launch_heads_join(const HeadsArgs &a, float *hend, const float *ldec, int reverse, hipStream_t s);
+hipError_t launch_heads_join(const HeadsArgs &a, int walks, hipStream_t s);
 hipError_t launch_heads_rows(const HeadsArgs &a, const float *from, float *to, hipStream_t s);
 hipError_t launch_heads_fwd(const HeadsArgs &a, hipStream_t s);
 hipError_t launch_heads_bwd(const HeadsArgs &a, hipStream_t s);

@@ -254,8 +254,10 @@ __global__ __launch_bounds__(512) void norm_reduce_kernel(NormArgs a) {
     const int x = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
     float v = 0.0f;
-    if (c < a.d)
+    if (c < a.d) {
+#pragma unroll 8
         for (int64_t r = w; r < a.nblk; r += 16) v += a.part[r * a.d + c];
+    }
     sum[w][x] = v;
     for (int n = 8; n > 0; n >>= 1) {
         __syncthreads();

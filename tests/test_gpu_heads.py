@@ -244,7 +244,8 @@ def test_same_bits_again_and_on_another_stream(dev, io):
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,H,P,G,N", [(1, 1, 1, 1, 1), (1, 4, 64, 1, 128), (5, 6, 33, 2, 24),
-                                          (3, 3, 48, 3, 101), (40, 80, 64, 1, 128), (2, 2, 256, 1, 256)])
+                                          (3, 3, 48, 3, 101), (40, 80, 64, 1, 128), (2, 2, 256, 1, 256),
+                                          (40, 16, 33, 2, 6), (20, 32, 200, 1, 101)])
 def test_update(dev, io, rows, H, P, G, N):
     say(f"update {io} {rows} {H} {P} {G} {N}")
     t = make(dev, io, rows, 1, H, P, G, N, seed=rows + N)
