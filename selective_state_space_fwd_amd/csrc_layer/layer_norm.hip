@@ -7,8 +7,8 @@
 // group of a row in registers, so the statistic (float32) and the scale need
 // no second read.  Measured: gated, 8 bits, 16384 x 5120, 422 MB in 95 us
 // (4.4 TB/s; the copy's rate would be 81); gated gradients, 8192 x 5120 in two
-// groups, 420 MB in 98 us (4.3 TB/s; a barrier a row) and 11 for dweight's partial
-// rows, where the copy's rate would be 81; 4 rows of 2560: 4 us, a launch.
+// groups, 420 MB in 84 us (5.0 TB/s) and 5 for dweight's partial rows, where the
+// copy's rate would be 81; 4 rows of 2560: 4 us, a launch.
 #include "layer_common.h"
 
 namespace ssm {
@@ -177,6 +177,35 @@ __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < VW; ++i) dw[k][i] = 0.0f;
+    // The next row on its way while this one is summed, and the weight kept,
+    // where there are registers for it (two vectors a lane: 84 against 99 us at
+    // 8192 x 5120 in two gated groups).
+    constexpr bool AHEAD = NV * VW <= 16;
+    Piece<RT, VW> xn[AHEAD ? NV : 1];
+    Piece<IO, VW> yn[AHEAD ? NV : 1], zn[AHEAD ? NV : 1];
+    float wk[AHEAD ? NV : 1][VW];
+    auto fetch = [&](int k, int64_t row, int64_t c) {
+        xn[k].load(static_cast<const R *>(a.x) + row * a.x_row + c);
+        yn[k].load(static_cast<const T *>(a.dy) + row * a.dy_row + c);
+        if (a.z) zn[k].load(static_cast<const T *>(a.z) + row * a.z_row + c);
+    };
+    auto weight = [&](int k, int64_t e, float (&w)[VW]) {
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < VW; ++i) w[i] = wk[k][i];
+        } else {
+            load_vec<F32, VW>(a.weight + g0 + e, w);
+        }
+    };
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+            if (e >= a.group) continue;
+            load_vec<F32, VW>(a.weight + g0 + e, wk[k]);
+            fetch(k, blockIdx.x, g0 + e);           // nblk <= rows
+        }
+    }
     int par = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += a.nblk, par ^= 1) {
         float s[NV][VW], z[NV][VW], dy[NV][VW], gate[NV][VW];
@@ -187,13 +216,18 @@ __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < VW; ++i) { s[k][i] = 0.0f; z[k][i] = 0.0f; dy[k][i] = 0.0f; gate[k][i] = 1.0f; }
             if (e < a.group) {
-                const int64_t c = g0 + e;
                 float w[VW];
-                load_vec<RT, VW>(static_cast<const R *>(a.x) + row * a.x_row + c, s[k]);
-                load_vec<IO, VW>(static_cast<const T *>(a.dy) + row * a.dy_row + c, dy[k]);
-                load_vec<F32, VW>(a.weight + c, w);
+                if constexpr (AHEAD) {
+                    xn[k].get(s[k]);
+                    yn[k].get(dy[k]);
+                } else {
+                    load_vec<RT, VW>(static_cast<const R *>(a.x) + row * a.x_row + g0 + e, s[k]);
+                    load_vec<IO, VW>(static_cast<const T *>(a.dy) + row * a.dy_row + g0 + e, dy[k]);
+                }
+                weight(k, e, w);
                 if (a.z) {
-                    load_vec<IO, VW>(static_cast<const T *>(a.z) + row * a.z_row + c, z[k]);
+                    if constexpr (AHEAD) zn[k].get(z[k]);
+                    else load_vec<IO, VW>(static_cast<const T *>(a.z) + row * a.z_row + g0 + e, z[k]);
 #pragma unroll
                     for (int i = 0; i < VW; ++i) gate[k][i] = silu_f32(z[k][i]);
                 }
@@ -204,6 +238,14 @@ __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
                     dot = __builtin_fmaf(dy[k][i] * w[i], g, dot);
                 }
             }
+        }
+        if constexpr (AHEAD) {
+            if (row + a.nblk < a.rows)
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const int64_t e = (static_cast<int64_t>(k) * blockDim.x + tid) * VW;
+                    if (e < a.group) fetch(k, row + a.nblk, g0 + e);
+                }
         }
         sq = wave_sum(sq);
         dot = wave_sum(dot);
@@ -222,7 +264,7 @@ __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
             if (e < a.group) {
                 const int64_t c = g0 + e;
                 float w[VW], dx[VW], dz[VW], dr[VW];
-                load_vec<F32, VW>(a.weight + c, w);
+                weight(k, e, w);
                 if (a.dresidual)
                     load_vec<RT, VW>(static_cast<const R *>(a.dresidual) + row * a.d + c, dr);
 #pragma unroll
