@@ -221,6 +221,11 @@ def test_norm_wide_rows(dev, io, d):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_norm_more_groups_than_a_grid_has_rows(dev, io):
+    check_norm(dev, io, 3, 140000, 2, None, True)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("pad,odd", [(8, 0), (1, 0), (0, 1), (3, 5)])
 def test_norm_strides_and_alignment(dev, io, pad, odd):
     check_norm(dev, io, 5, 264, 132, "f32", True, pad=pad, odd=odd)
