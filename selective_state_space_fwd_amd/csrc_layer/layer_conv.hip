@@ -7,10 +7,10 @@
 // neighbouring channels and walks a run of tokens with the last W - 1 inputs
 // in registers; the runs' W - 1 overlapping tokens come from the caches.
 // Measured, 5376 channels of width 4 in bfloat16: 8 x 2048 tokens 353 MB in 80
-// us (4.4 TB/s; a copy of as much takes 68), gradients of 4 x 2048 264 MB in 69
-// us (3.8 TB/s; v is made again, and silu' takes an exponential and a reciprocal
-// a value) and 8 for the sums over the runs; a token of 256 rows in float32, 44
-// MB, in 12 us.
+// us (4.4 TB/s; a copy of as much takes 68), gradients of 4 x 2048 264 MB in 72
+// us with the sums over the runs (3.7 TB/s; v is made again, and silu' takes an
+// exponential and a reciprocal a value); a token of 256 rows in float32, 44 MB,
+// in 12 us.
 #include "layer_common.h"
 
 namespace ssm {
@@ -143,13 +143,13 @@ template <class IO, int VW, int W>
 __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvArgs a) {
     using T = typename IO::T;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x) * VW;
-    const int64_t per = (a.L + kConvBwdRun - 1) / kConvBwdRun;
+    const int64_t per = (a.L + a.run - 1) / a.run;
     if (c >= a.C) return;
     Taps<IO, VW, W> k;
     k.load(a, c);
     for (int64_t id = blockIdx.y; id < a.runs; id += gridDim.y) {
-        const int64_t b = id / per, t0 = (id % per) * kConvBwdRun;
-        const int64_t t1 = t0 + kConvBwdRun < a.L ? t0 + kConvBwdRun : a.L;
+        const int64_t b = id / per, t0 = (id % per) * a.run;
+        const int64_t t1 = t0 + a.run < a.L ? t0 + a.run : a.L;
         float dw[W][VW], db[VW];
 #pragma unroll
         for (int i = 0; i < VW; ++i) {

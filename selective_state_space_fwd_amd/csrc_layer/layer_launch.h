@@ -28,13 +28,12 @@ struct ConvArgs {
     float *dweight, *dbias;     // (C, W), (C)
     float *dstate;              // (rows, C, W-1) or null
     float *part;                // workspace: (runs, W + 1, C)
-    int64_t runs;
+    int64_t runs, run;          // a batch row's run of `run` tokens leaves one partial row
     // single token
     float *slot_state;          // (n_slots, C, W-1)
     const int32_t *slots;       // (batch) or null: row i is slot i
     int64_t n_slots;
 };
-constexpr int kConvBwdRun = 32;  // tokens of one backward run (one partial sum of dweight)
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_update(const ConvArgs &a, hipStream_t s);
