@@ -6,8 +6,8 @@
 // far below the vector rate, so HBM bounds them.  A lane owns four
 // neighbouring channels and walks a run of tokens with the last W - 1 inputs
 // in registers; the runs' W - 1 overlapping tokens come from the caches.
-// Measured, 5376 channels of width 4 in bfloat16: 8 x 2048 tokens 353 MB in 80
-// us (4.4 TB/s; a copy of as much takes 68), gradients of 4 x 2048 264 MB in 72
+// Measured, 5376 channels of width 4 in bfloat16: 8 x 2048 tokens 353 MB in 76
+// us (4.6 TB/s; a copy of as much takes 68), gradients of 4 x 2048 264 MB in 72
 // us with the sums over the runs (3.7 TB/s; v is made again, and silu' takes an
 // exponential and a reciprocal a value); a token of 256 rows in float32, 44 MB,
 // in 12 us.
@@ -56,19 +56,18 @@ __device__ __forceinline__ void input_at(const ConvArgs &a, const SeqRun &q, int
         o[i] = a.state && k >= 0 ? a.state[(q.row * a.C + c + i) * (W - 1) + k] : 0.0f;
 }
 
-constexpr int kFwdRun = 16;     // tokens a lane walks in the forward pass
-
-template <class IO, int VW, int W>
+// RUN: tokens a lane walks.
+template <class IO, int VW, int W, int RUN>
 __global__ __launch_bounds__(64) void conv_fwd_kernel(ConvArgs a) {
     using T = typename IO::T;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x) * VW;
-    const int64_t nrun = (a.L + kFwdRun - 1) / kFwdRun;
+    const int64_t nrun = (a.L + RUN - 1) / RUN;
     if (c >= a.C) return;
     Taps<IO, VW, W> k;
     k.load(a, c);
     for (int64_t id = blockIdx.y; id < a.batch * nrun; id += gridDim.y) {
-        const int64_t b = id / nrun, t0 = (id % nrun) * kFwdRun;
-        const int64_t t1 = t0 + kFwdRun < a.L ? t0 + kFwdRun : a.L;
+        const int64_t b = id / nrun, t0 = (id % nrun) * RUN;
+        const int64_t t1 = t0 + RUN < a.L ? t0 + RUN : a.L;
         int64_t t = t0;
         while (t < t1) {
             const SeqRun q = seq_run(a, b, t);
@@ -79,12 +78,12 @@ __global__ __launch_bounds__(64) void conv_fwd_kernel(ConvArgs a) {
             for (int j = 1; j < W; ++j) input_at<IO, VW, W>(a, q, b, t - W + j, c, h[j]);
             // the run's tokens all on their way before the first is used
             const T *x = static_cast<const T *>(a.x) + b * a.x_batch + t * a.x_token + c;
-            Piece<IO, VW> in[kFwdRun];
+            Piece<IO, VW> in[RUN];
 #pragma unroll
-            for (int n = 0; n < kFwdRun; ++n)
+            for (int n = 0; n < RUN; ++n)
                 if (t + n < e) in[n].load(x + n * a.x_token);
 #pragma unroll
-            for (int n = 0; n < kFwdRun; ++n) {
+            for (int n = 0; n < RUN; ++n) {
                 if (t + n < e) {
 #pragma unroll
                     for (int j = 0; j + 1 < W; ++j)
@@ -367,12 +366,23 @@ static bool conv_vec(const ConvArgs &a, bool bwd) {
     return ok && (!a.slot_state || al16(a.slot_state));
 }
 
+template <class IO, int VW, int W, int RUN>
+static void conv_fwd_run(const ConvArgs &a, unsigned gx, hipStream_t s) {
+    const int64_t runs = a.batch * ((a.L + RUN - 1) / RUN);
+    if (runs > 0)
+        hipLaunchKernelGGL((conv_fwd_kernel<IO, VW, W, RUN>), dim3(gx, grid_y(runs)), dim3(64), 0, s, a);
+}
+
+// Runs of 24 tokens where their 8-byte pieces fit the registers and leave eight
+// wavefronts a SIMD to come; else of 16 (8 x 2048 x 5376 in bfloat16: 76 against
+// 82 us, x 1024: 19.5 against 17.7; 4 x 2048 x 5376 in float32: 74 against 69).
 template <class IO, int VW, int W>
 static hipError_t conv_fwd_w(const ConvArgs &a, hipStream_t s) {
     const unsigned gx = static_cast<unsigned>((a.C + 64 * VW - 1) / (64 * VW));
-    const int64_t runs = a.batch * ((a.L + kFwdRun - 1) / kFwdRun);
-    if (runs > 0)
-        hipLaunchKernelGGL((conv_fwd_kernel<IO, VW, W>), dim3(gx, grid_y(runs)), dim3(64), 0, s, a);
+    if (sizeof(typename IO::T) * VW == 8 && gx * a.batch * (a.L / 24) >= 8192)
+        conv_fwd_run<IO, VW, W, sizeof(typename IO::T) * VW == 8 ? 24 : 16>(a, gx, s);
+    else
+        conv_fwd_run<IO, VW, W, 16>(a, gx, s);
     if (W > 1 && a.last && (a.cu || a.L == 0) && a.rows > 0)
         hipLaunchKernelGGL(conv_empty_kernel, dim3(4, grid_y(a.rows)), dim3(256), 0, s, a.cu, a.L,
                            a.rows, a.C * (W - 1), a.state, a.last);

@@ -99,9 +99,10 @@ def test_conv_channels_and_strides(dev, io, ch, pad, odd):
     check_conv(dev, io, 2, 40, ch, 4, pad=pad, odd=odd)
 
 
-@pytest.mark.parametrize("io,lens", [("f32", [1000, 0, 63, 64, 973]), ("bf16", [2000, 1, 129, 2860])])
+@pytest.mark.parametrize("io,lens", [("f32", [1000, 0, 63, 64, 973]), ("bf16", [2000, 1, 129, 2860]),
+                                     ("bf16", [3001, 23, 24, 2960])])
 def test_conv_many_channels(dev, io, lens):
-    """Gradients in runs of 32 and of 64 tokens, sequences ending inside them."""
+    """Runs of 24 tokens, and of 32 and 64 in the gradients; sequences end inside them."""
     check_conv(dev, io, 1, sum(lens), 8196, 4, lens=lens)
 
 
