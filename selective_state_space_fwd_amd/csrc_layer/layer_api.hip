@@ -50,7 +50,7 @@ struct HeadsPlan {
     int64_t nc = 0, Kc = 1, J = 1, wgs = 0, sph = 0, rows = 0;
     int64_t hsplit = 1, hblk = 1, na = 0;
     size_t table = 0, hend = 0, ldec = 0, hin = 0, gout = 0, rp = 0, rpsum = 0, hdot = 0, through = 0,
-           anchor = 0, adot = 0, rec = 0, part = 0, dBp = 0, dCp = 0, bytes = 0;
+           rest = 0, adot = 0, rec = 0, part = 0, dBp = 0, dCp = 0, bytes = 0;
 };
 
 // A walk is serial over its chunks, and a compute unit holds three of its
@@ -118,7 +118,7 @@ ssm_status plan_heads(const ssm_heads_desc *d, bool bwd, HeadsPlan *p) {
         p->rpsum = take(2.0 * chunks * slices, 4);
         p->hdot = take(p->rows * slices, 4);
         p->na = ceil_div(p->nc, ssm::kAnchor);
-        p->anchor = take(2.0 * d->batch * p->na * slices * 16 * ssm::heads_np(d->d_state), 4);
+        if (bf16) p->rest = take(2.0 * d->batch * p->na * slices * 16 * ssm::heads_np(d->d_state), 2);
         p->adot = take(static_cast<double>(d->batch) * p->na * d->heads, 4);
         p->through = take(static_cast<double>(chunks) * d->heads, 4);
         p->rec = take(static_cast<double>(chunks) * d->heads, ssm::kGradRec);
@@ -153,7 +153,7 @@ void heads_args(const ssm_heads_desc *d, const HeadsPlan &p, bool bwd, ssm::Head
     if (!bwd) return;
     a->hin = w + p.hin; a->gout = w + p.gout;
     a->rp = f(p.rp); a->rpsum = f(p.rpsum); a->hdot = f(p.hdot); a->through = f(p.through);
-    a->anchor = f(p.anchor); a->adot = f(p.adot); a->na = p.na;
+    a->rest = reinterpret_cast<uint16_t *>(f(p.rest)); a->adot = f(p.adot); a->na = p.na;
     a->rec = w + p.rec; a->part = f(p.part); a->dBp = f(p.dBp); a->dCp = f(p.dCp);
 }
 

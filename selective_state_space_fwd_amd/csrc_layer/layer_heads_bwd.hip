@@ -15,8 +15,8 @@
 // and X needs no product of its own: a chunk's X plus its p is <gh, h> at its
 // end, which is the next chunk's X plus that one's r.  The rounding errors of
 // r and p gather along the way, and alike for all tokens behind, so they do
-// not cancel in dA: every kAnchor-th chunk X is taken anew from float32 copies
-// of the states.
+// not cancel in dA: every kAnchor-th chunk X is taken anew from its states, which
+// have the rest of their float32 bits beside them there.
 //
 // Two walks, one in each direction and both in one launch, keep the state (or
 // gh) in registers and leave it at every chunk, with r and p, which go into
@@ -24,11 +24,11 @@
 // chunk is on its own: a workgroup takes a chunk of a group, loops over its
 // heads, and sums dB and dC over them in registers, in a fixed order.
 //
-// 4 x 2048 x 80 heads x 64, 128 states, bfloat16: 566 us (walks 310, anchors 57,
-// chunks 195, decays 28, the rest 18 by a profiler's clock), against 50 for 263
-// MB at a copy's rate.  What bounds it: the states go through memory, 0.67 GB
-// written by the walks and read by the two launches behind them, 1.3 GB or 260
-// us; that is the price of chunks that do not wait for each other, without which
+// 4 x 2048 x 80 heads x 64, 128 states, bfloat16: 533 us (walks 315, products of
+// the states 51, chunks 200, decays 29, the rest 14 by a profiler's clock), against
+// 50 for 263 MB at a copy's rate.  What bounds it: the states go through memory,
+// 0.5 GB written by the walks and 0.67 read by the two launches behind them, about
+// 220 us; that is the price of chunks that do not wait for each other, without which
 // 640 walks of everything would be all the parallel work there is.  The rest is
 // the steps of a chunk behind one another, as in the forward walk.  Float32 at
 // the same sizes: 1280 us.
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
     const int64_t slot0 = (dir * a.batch + b) * a.nc * slices + slice;
     E *left = static_cast<E *>(dir ? a.gout : a.hin) + (b * a.nc * slices + slice) * NT * 256;
     float *rp0 = a.rp + slot0 * Q, *rpsum0 = a.rpsum + slot0;
-    float *anchor0 = a.anchor + ((dir * a.batch + b) * a.na * slices + slice) * NT * 256;
+    uint16_t *rest0 = a.rest + ((dir * a.batch + b) * a.na * slices + slice) * NT * 256;
 
     f4 S[NT];
     auto state_at = [&](int N_, int nt, int i) -> uint32_t {
@@ -296,8 +296,8 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
             const Rsrc to = view(left + c * slices * (NT * 256), idle ? 0 : NT * 256 * ES);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) M::store(M::half(S[nt]), to, lane * 4 * ES, nt * 256 * ES);
-            if (!idle) {
-                if (sizeof(E) == 2 && k.first) {
+            if constexpr (sizeof(E) == 2) {
+                if (!idle && k.first) {
                     // X of a first chunk needs the product with the start state
                     const ArgsAgain again = args_again();
                     if (dir == 1 && again->h0) {
@@ -313,12 +313,13 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
                         for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
                         if (lane == 0) again->hdot[k.row * slices + slice] = v;
                     }
-                } else if (sizeof(E) == 2 && c % kAnchor == 0 && dec >= kDirect) {
-                    const Rsrc an = view(anchor0 + c / kAnchor * slices * (NT * 256), NT * 256 * 4);
+                } else if (!idle && c % kAnchor == 0 && dec >= kDirect) {
+                    const Rsrc an = view(rest0 + c / kAnchor * slices * (NT * 256), NT * 256 * 2);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) store16(S[nt], an, lane * 16, nt * 1024);
+                    for (int nt = 0; nt < NT; ++nt)
+                        M::store(M::rest(S[nt], M::half(S[nt])), an, lane * 8, nt * 512);
                 }
-                if (sizeof(E) == 2 && dir == 0 && p0 == 0 && lane == 0)
+                if (dir == 0 && p0 == 0 && lane == 0 && !idle)
                     a.through[(static_cast<int64_t>(b) * a.nc + c) * H + h] = dec;
             }
             // ---- and dot it with the other side's tokens: channels by tokens
@@ -402,20 +403,32 @@ __global__ __launch_bounds__(256, (walk_waves<IO, NP, Q, FULL>())) void heads_wa
 }
 
 // <gh, h_in> of every kAnchor-th chunk that keeps kDirect, a workgroup a head;
-// of no meaning, and not used, where a sequence begins.  A stream: 336 MB in 57
-// us (5.9 TB/s) at 4 x 2048 x 80 heads.
+// of no meaning, and not used, where a sequence begins.  A stream: 336 MB in 51
+// us (6.6 TB/s) at 4 x 2048 x 80 heads.
 __global__ __launch_bounds__(256) void heads_anchor_kernel(HeadsArgs a, int np) {
     const int64_t h = blockIdx.x % a.H, x = blockIdx.x / a.H;      // x: batch row and anchor
-    const int64_t sph = (a.P + 15) / 16, per = sph * 4 * np;       // f4s of one head
+    const int64_t sph = (a.P + 15) / 16, per = sph * 2 * np;       // 8 values of one head each
     const int64_t all = a.batch * a.na * a.H * per;
     const int64_t c = x / a.na * a.nc + x % a.na * kAnchor;
     if (a.through[c * a.H + h] < kDirect) return;
-    const f4 *p = reinterpret_cast<const f4 *>(a.anchor) + (x * a.H + h) * per;
+    const uint4 *s0 = static_cast<const uint4 *>(a.hin) + (c * a.H + h) * per;
+    const uint4 *s1 = static_cast<const uint4 *>(a.gout) + (c * a.H + h) * per;
+    const uint4 *r0 = reinterpret_cast<const uint4 *>(a.rest) + (x * a.H + h) * per;
     __shared__ double sum[4];
     double v = 0.0;
     for (int64_t i = threadIdx.x; i < per; i += 256) {
-        const f4 q = p[i] * p[all + i];
-        v += static_cast<double>((q.x + q.y) + (q.z + q.w));
+        const uint4 p = s0[i], q = s1[i], pr = r0[i], qr = r0[all + i];
+        const uint32_t ps[4] = {p.x, p.y, p.z, p.w}, qs[4] = {q.x, q.y, q.z, q.w};
+        const uint32_t pt[4] = {pr.x, pr.y, pr.z, pr.w}, qt[4] = {qr.x, qr.y, qr.z, qr.w};
+        float w = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float p0, p1, q0, q1;
+            Mat<BF16>::whole(ps[e], pt[e], p0, p1);
+            Mat<BF16>::whole(qs[e], qt[e], q0, q1);
+            w += __builtin_fmaf(p0, q0, p1 * q1);
+        }
+        v += static_cast<double>(w);
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);

@@ -60,7 +60,7 @@ int64_t norm_bwd_blocks(int64_t rows, int64_t d, int64_t group);
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s);
 
-// Chunks between two float32 copies of the states in the backward (bfloat16).
+// Every kAnchor-th chunk of the backward has its states in all 32 bits (bfloat16).
 // At 4 x 2048 x 80 heads dA is off by 3e-7 of its norm with 2; with 4 by 1.4e-6
 // for 50 us of 570 less, and a sharper head's up to 3e-6 with 8.
 constexpr int kAnchor = 2;
@@ -100,8 +100,8 @@ struct HeadsArgs {
     float *rp;                  // (2, batch nc, H slices, Q) dot products across chunks, see layer_heads_bwd.hip
     float *rpsum;               // (2, batch nc, H slices) their sums over a chunk's tokens
     float *hdot;                // (rows, H slices) <gradient leaving a first chunk, start state>
-    float *anchor;              // (2, batch, na, H slices, 16 Np) float32 state entering every
-                                // kAnchor-th chunk, and gradient leaving it
+    uint16_t *rest;             // (2, batch, na, H slices, 16 Np) low halves of every kAnchor-th
+                                // chunk's states (bfloat16 I/O; hin and gout hold the high ones)
     float *adot;                // (batch, na, H) their products
     int64_t na;
     float *through;             // (batch nc, H) exp(s_Q) <gout, hin>

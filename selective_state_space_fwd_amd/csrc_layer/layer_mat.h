@@ -116,6 +116,21 @@ struct Mat<BF16> {
         __builtin_amdgcn_raw_buffer_store_b64(u2{h.x, h.y}, to, off, more, 0);
     }
     static __device__ __forceinline__ Half none() { return make_uint2(0, 0); }
+    // What the rounding of v to h left of the float32 bits, in 16 bits: with h
+    // all of v again.  (A tie rounded down leaves 0x8000, one too many: 2^-24.)
+    static __device__ __forceinline__ Half rest(f4 v, Half h) {
+        auto two = [](float a, float b, uint32_t h2) {
+            const int x = min(static_cast<int>(__float_as_uint(a) - (h2 << 16)), 0x7fff);
+            const int y = min(static_cast<int>(__float_as_uint(b) - (h2 & 0xffff0000u)), 0x7fff);
+            return __builtin_amdgcn_perm(static_cast<uint32_t>(y), static_cast<uint32_t>(x), 0x05040100);
+        };
+        return make_uint2(two(v.x, v.y, h.x), two(v.z, v.w, h.y));
+    }
+    // two values of h and what their rounding left
+    static __device__ __forceinline__ void whole(uint32_t h, uint32_t r, float &a, float &b) {
+        a = __uint_as_float((h << 16) + static_cast<uint32_t>(static_cast<int>(r << 16) >> 16));
+        b = __uint_as_float((h & 0xffff0000u) + static_cast<uint32_t>(static_cast<int>(r) >> 16));
+    }
     static __device__ __forceinline__ Frag join(Half a, Half b) {
         Bits x;
         x.d[0] = a;
