@@ -25,7 +25,7 @@
 // heads, and sums dB and dC over them in registers, in a fixed order.
 //
 // 4 x 2048 x 80 heads x 64, 128 states, bfloat16: 533 us (walks 315, products of
-// the states 51, chunks 200, decays 29, the rest 14 by a profiler's clock), against
+// the states 51, chunks 197, decays 21, the rest 14 by a profiler's clock), against
 // 50 for 263 MB at a copy's rate.  What bounds it: the states go through memory,
 // 0.5 GB written by the walks and 0.67 read by the two launches behind them, about
 // 220 us; that is the price of chunks that do not wait for each other, without which
@@ -970,8 +970,8 @@ heads_chunk_bwd_kernel(HeadsArgs a, GradRec<Q> *rec) {
 // wavefront a head, a lane a token.  E comes without differences of long sums:
 // of the tiles (q, r) of Z those with r < own < q count whole, those of the own
 // row from the token on, those of the own column up to it; only the tile on
-// the diagonal is a difference.  28 us at 4 x 2048 x 80 heads: 1.8 KB a chunk and
-// head, read in pieces of 64 bytes.
+// the diagonal is a difference.  21 us at 4 x 2048 x 80 heads (28 with the loads
+// one behind another): 1.8 KB a chunk and head, and single values of delta.
 template <class IO, int Q>
 __global__ __launch_bounds__(256) void heads_grad_kernel(HeadsArgs a, const GradRec<Q> *rec) {
     using E = typename IO::T;
@@ -999,24 +999,21 @@ __global__ __launch_bounds__(256) void heads_grad_kernel(HeadsArgs a, const Grad
     const GradRec<Q> &rc = rec[id];
     float cv = 0.0f, dd = 0.0f, r = 0.0f, p = 0.0f;
     double rows = 0.0, cols = 0.0, whole = 0.0;
-    if (lane < Q) {
-        const int dg = own * (own + 1) / 2 + own;
-        for (int q = own + 1; q < TT; ++q) {
-            const int at = q * (q + 1) / 2;
-            cv += rc.colv[(at + own) * 16 + l];
-            for (int x = 0; x < own; ++x)
-                for (int i = 0; i < 16; i += 4) {
-                    const f4 w = *reinterpret_cast<const f4 *>(rc.rowz + (at + x) * 16 + i);
-                    whole += (w.x + w.y) + (w.z + w.w);
-                }
-        }
-        cols = static_cast<double>(cv) * dt;
-        for (int x = 0; x < own; ++x) rows += rc.rowz[(own * (own + 1) / 2 + x) * 16 + l];
-        rows += static_cast<double>(rc.rowz[dg * 16 + l]) -
-                static_cast<double>(rc.colv[dg * 16 + l] - rc.diagz[lane]) * dt;
-        cv += rc.colv[dg * 16 + l];
+    // all loads without a branch between them; a lane's own row and column of tiles
+    const bool in = lane < Q;
+    float rz[TT], cz[TT], tz[TT][TT];
+#pragma unroll
+    for (int x = 0; x < TT; ++x) {
+        rz[x] = in && x <= own ? rc.rowz[(own * (own + 1) / 2 + x) * 16 + l] : 0.0f;
+        cz[x] = in && x >= own ? rc.colv[(x * (x + 1) / 2 + own) * 16 + l] : 0.0f;
+#pragma unroll
+        for (int y = 0; y + 1 < x; ++y) tz[x][y] = rc.rowz[(x * (x + 1) / 2 + y) * 16 + l];
+    }
+    const float diagz = in ? rc.diagz[lane] : 0.0f;
+    if (in) {
         dd = rc.diag[lane];
         const float *rp = a.rp + (ci * slices + h * sph) * Q + lane;
+#pragma unroll 4
         for (int64_t i = 0; i < sph; ++i) {
             r += rp[i * Q];
             p += rp[chunks * slices * Q + i * Q];
@@ -1024,6 +1021,21 @@ __global__ __launch_bounds__(256) void heads_grad_kernel(HeadsArgs a, const Grad
         r *= exp2_d(s);
         p *= exp2_d(sQ - s);
     }
+    float dr_ = 0.0f, dc_ = 0.0f;               // of the tile on the diagonal
+#pragma unroll
+    for (int x = 0; x < TT; ++x) {
+        if (x < own) rows += rz[x];
+        if (x > own) cv += cz[x];
+        if (x == own) { dr_ = rz[x]; dc_ = cz[x]; }
+#pragma unroll
+        for (int y = 0; y + 1 < x; ++y) {
+            const float all = row_sum(tz[x][y]);
+            if (in && y < own && own < x) whole += all;
+        }
+    }
+    cols = static_cast<double>(cv) * dt;
+    rows += static_cast<double>(dr_) - static_cast<double>(dc_ - diagz) * dt;
+    cv += dc_;
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) {      // rows: from the token on; columns: up to it
         const double x = __shfl_down(rows, o, 16), y = __shfl_up(cols, o, 16);
