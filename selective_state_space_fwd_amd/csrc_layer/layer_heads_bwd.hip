@@ -24,7 +24,7 @@
 // chunk is on its own: a workgroup takes a chunk of a group, loops over its
 // heads, and sums dB and dC over them in registers, in a fixed order.
 //
-// 4 x 2048 x 80 heads x 64, 128 states, bfloat16: 533 us (walks 315, products of
+// 4 x 2048 x 80 heads x 64, 128 states, bfloat16: 526 us (walks 315, products of
 // the states 51, chunks 197, decays 21, the rest 14 by a profiler's clock), against
 // 50 for 263 MB at a copy's rate.  What bounds it: the states go through memory,
 // 0.5 GB written by the walks and 0.67 read by the two launches behind them, about
